@@ -18,6 +18,9 @@ Tensor conventions (all contiguous, on the current CUDA device):
   conv_w               [3*H*D, 4]      float32
   conv cache           [N, 3, 3*H*D]   activation dtype, oldest row first
   cu_seqlens           [N+1]           int32
+
+Gated delta rule with one decay per head (``kda_gdr_*``): q, k [T, HK, D], v, o [T, HV, D],
+g and beta [T, HV] float32, states [N, HV, D, D] float32, HV a multiple of HK.
 """
 from __future__ import annotations
 
@@ -35,6 +38,16 @@ __all__ = [
     "kda_chunk_fwd_windowed_workspace_bytes",
     "kda_decode_step",
     "kda_prologue_chunk_fwd",
+    "kda_gdr_recurrent",
+    "kda_gdr_decode_step",
+    "kda_gdr_chunk_fwd",
+    "kda_gdr_chunk_fwd_workspace_bytes",
+    "kda_gdr_chunk_bwd",
+    "kda_gdr_chunk_bwd_workspace_bytes",
+    "kda_prologue_bwd",
+    "kda_prologue_bwd_workspace_bytes",
+    "kda_output_epilogue_bwd",
+    "kda_output_epilogue_bwd_workspace_bytes",
     "kda_get_device_status",
     "kda_selftest_wait_timeout",
     "kda_selftest_bounds",
@@ -123,6 +136,21 @@ lib.kda_chunk_fwd_windowed_workspace_bytes.restype = ctypes.c_size_t
 lib.kda_decode_step.argtypes = [_vp, _vp, _vp, _vp, _vp, _f, _vp, _i, _i, _i, _i, _vp, _vp]
 lib.kda_prologue_chunk_fwd.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _f, _vp, _vp, _i, _i, _i,
                                        _i, _i, _vp, _vp, _vp]
+lib.kda_gdr_recurrent.argtypes = [_vp] * 5 + [_f, _vp, _vp] + [_i] * 6 + [_vp] * 3
+lib.kda_gdr_decode_step.argtypes = [_vp] * 5 + [_f, _vp] + [_i] * 5 + [_vp] * 2
+lib.kda_gdr_chunk_fwd_ws.argtypes = ([_vp] * 5 + [_f, _vp, _vp] + [_i] * 6
+                                     + [_vp] * 3 + [ctypes.c_size_t, _vp])
+lib.kda_gdr_chunk_bwd_ws.argtypes = ([_vp] * 5 + [_f, _vp, _vp] + [_i] * 6
+                                     + [_vp] * 9 + [ctypes.c_size_t, _vp])
+lib.kda_prologue_bwd.argtypes = [_vp] * 4 + [_i] * 6 + [_vp] * 7 + [ctypes.c_size_t, _vp]
+lib.kda_output_epilogue_bwd.argtypes = ([_vp] * 3 + [_f, _vp] + [_i] * 4 + [_vp] * 4
+                                        + [ctypes.c_size_t, _vp])
+for _fn, _n in ((lib.kda_gdr_chunk_fwd_workspace_bytes, 6),
+                (lib.kda_gdr_chunk_bwd_workspace_bytes, 6),
+                (lib.kda_prologue_bwd_workspace_bytes, 5),
+                (lib.kda_output_epilogue_bwd_workspace_bytes, 3)):
+    _fn.argtypes = [_i] * _n
+    _fn.restype = ctypes.c_size_t
 lib.kda_get_device_status.argtypes = [ctypes.POINTER(ctypes.c_int)]
 lib.kda_selftest_wait_timeout.argtypes = [ctypes.c_uint, _vp]
 lib.kda_selftest_bounds.argtypes = [_i, _vp]
@@ -135,7 +163,9 @@ for _fn in (lib.kda_prologue, lib.kda_chunk_fwd, lib.kda_chunk_fwd_ws, lib.kda_c
             lib.kda_state_compose,
             lib.kda_prologue_chunk_fwd_ws, lib.kda_decode_step, lib.kda_chunk_fwd_gated_ws,
             lib.kda_prologue_chunk_fwd_gated_ws, lib.kda_decode_step_gated,
-            lib.kda_output_epilogue,
+            lib.kda_output_epilogue, lib.kda_gdr_recurrent, lib.kda_gdr_decode_step,
+            lib.kda_gdr_chunk_fwd_ws, lib.kda_gdr_chunk_bwd_ws, lib.kda_prologue_bwd,
+            lib.kda_output_epilogue_bwd,
             lib.kda_prologue_chunk_fwd, lib.kda_get_device_status,
             lib.kda_selftest_wait_timeout, lib.kda_selftest_bounds):
     _fn.restype = ctypes.c_int
@@ -615,3 +645,202 @@ def kda_output_epilogue(o, gate, weight, out, *, eps: float = 1e-5, stream=None)
     T, H, D = o.shape
     _check(lib.kda_output_epilogue(_ptr(o), _ptr(gate), _ptr(weight), float(eps), T, H, D,
                                    _dtype(out), _ptr(out), _stream(stream)))
+
+
+# ---- gated delta rule with one decay per head; backward of prologue and epilogue ----------
+# These functions check shapes as well: the kernels trust the sizes they are given.
+
+def _expect(device, *tensors):
+    """Each of (tensor, name, shape, dtype) is a contiguous tensor of that shape and dtype on
+    ``device``, the current CUDA device; a tensor that is None is left out."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be CUDA tensors, got {device}")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    for t, name, shape, dtype in tensors:
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _gdr_sizes(q, v, cu_seqlens):
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v have three dimensions: tokens, heads, channels")
+    T, HK, D = q.shape
+    return 1 if cu_seqlens is None else cu_seqlens.numel() - 1, T, HK, v.shape[1], D
+
+
+def _gdr_expect(q, k, v, g, beta, cu_seqlens, N, T, HK, HV, D, *more):
+    f32 = torch.float32
+    _expect(q.device, (q, "q", (T, HK, D), q.dtype), (k, "k", (T, HK, D), q.dtype),
+            (v, "v", (T, HV, D), q.dtype), (g, "g", (T, HV), f32), (beta, "beta", (T, HV), f32),
+            (cu_seqlens, "cu_seqlens", (N + 1,), torch.int32), *more)
+
+
+def _workspace(workspace, nbytes, device):
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    if workspace is not None:
+        _expect(device, (workspace, "workspace", workspace.shape, torch.uint8))
+    return workspace, 0 if workspace is None else workspace.numel()
+
+
+def kda_gdr_recurrent(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=None,
+                      final_state=None, cu_seqlens=None, stream=None):
+    """Gated delta rule with one decay per head, token by token: writes ``o`` [T, HV, D] and
+    optionally ``final_state`` (which may be ``initial_state``)."""
+    N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
+    f32, sq = torch.float32, (N, HV, D, D)
+    _gdr_expect(q, k, v, g, beta, cu_seqlens, N, T, HK, HV, D, (o, "o", (T, HV, D), f32),
+                (initial_state, "initial_state", sq, f32), (final_state, "final_state", sq, f32))
+    _check(lib.kda_gdr_recurrent(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
+                                 _ptr(initial_state), _ptr(cu_seqlens), N, T, HK, HV, D, _dtype(q),
+                                 _ptr(o), _ptr(final_state), _stream(stream)))
+
+
+def kda_gdr_decode_step(q, k, v, g, beta, state, o, *, scale: float = 1.0, stream=None):
+    """One new token for each of N sequences (``q, k`` [N, HK, D], ``v, o`` [N, HV, D]);
+    updates ``state`` [N, HV, D, D] in place."""
+    N, _, HK, HV, D = _gdr_sizes(q, v, None)
+    N = q.shape[0]
+    f32 = torch.float32
+    _gdr_expect(q, k, v, g, beta, None, N, N, HK, HV, D, (o, "o", (N, HV, D), f32),
+                (state, "state", (N, HV, D, D), f32))
+    _check(lib.kda_gdr_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
+                                   _ptr(state), N, HK, HV, D, _dtype(q), _ptr(o), _stream(stream)))
+
+
+def kda_gdr_chunk_fwd_workspace_bytes(N: int, T: int, HK: int, HV: int, D: int,
+                                      dtype: torch.dtype) -> int:
+    """Scratch bytes of :func:`kda_gdr_chunk_fwd` (0: it runs the recurrent form)."""
+    return int(lib.kda_gdr_chunk_fwd_workspace_bytes(N, T, HK, HV, D, _DTYPES[dtype]))
+
+
+def kda_gdr_chunk_fwd(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=None,
+                      final_state=None, cu_seqlens=None, workspace="auto", stream=None):
+    """Chunkwise prefill of the gated delta rule with one decay per head: writes ``o``
+    [T, HV, D] and optionally ``final_state``.
+
+    ``workspace``: ``"auto"`` takes the scratch from torch's caching allocator; a uint8 CUDA
+    tensor of :func:`kda_gdr_chunk_fwd_workspace_bytes` is used as given; ``None`` runs
+    :func:`kda_gdr_recurrent`.  fp32 inputs and D below 64 run the recurrent form."""
+    N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
+    f32, sq = torch.float32, (N, HV, D, D)
+    _gdr_expect(q, k, v, g, beta, cu_seqlens, N, T, HK, HV, D, (o, "o", (T, HV, D), f32),
+                (initial_state, "initial_state", sq, f32), (final_state, "final_state", sq, f32))
+    dt = _dtype(q)
+    nbytes = 0
+    if isinstance(workspace, str):
+        nbytes = int(lib.kda_gdr_chunk_fwd_workspace_bytes(N, T, HK, HV, D, dt))
+    workspace, nbytes = _workspace(workspace, nbytes, q.device)
+    _check(lib.kda_gdr_chunk_fwd_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
+                                    _ptr(initial_state), _ptr(cu_seqlens), N, T, HK, HV, D, dt,
+                                    _ptr(o), _ptr(final_state), _ptr(workspace), nbytes,
+                                    _stream(stream)))
+
+
+def kda_gdr_chunk_bwd_workspace_bytes(N: int, T: int, HK: int, HV: int, D: int,
+                                      dtype: torch.dtype) -> int:
+    """Scratch bytes of :func:`kda_gdr_chunk_bwd` (0 for sizes and types it does not have)."""
+    return int(lib.kda_gdr_chunk_bwd_workspace_bytes(N, T, HK, HV, D, _DTYPES[dtype]))
+
+
+def kda_gdr_chunk_bwd(q, k, v, g, beta, d_o, *, scale: float = 1.0, initial_state=None,
+                      d_final_state=None, cu_seqlens=None, dq=None, dk=None, dv=None, dg=None,
+                      dbeta=None, d_initial_state=None, want_d_initial_state=True,
+                      workspace="auto", stream=None):
+    """Gradients of :func:`kda_gdr_chunk_fwd` for L = sum(d_o * o) + sum(d_final_state *
+    final_state).  Returns ``(dq, dk, dv, dg, dbeta, d_initial_state)``: the first three of q's
+    dtype, the others fp32, the last None unless wanted; outputs not given are allocated."""
+    N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
+    f32, sq = torch.float32, (N, HV, D, D)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    dg = torch.empty_like(g) if dg is None else dg
+    dbeta = torch.empty_like(beta) if dbeta is None else dbeta
+    if d_initial_state is None and want_d_initial_state:
+        d_initial_state = torch.empty(sq, dtype=f32, device=q.device)
+    _gdr_expect(q, k, v, g, beta, cu_seqlens, N, T, HK, HV, D, (d_o, "d_o", (T, HV, D), f32),
+                (initial_state, "initial_state", sq, f32),
+                (d_final_state, "d_final_state", sq, f32), (dq, "dq", (T, HK, D), q.dtype),
+                (dk, "dk", (T, HK, D), q.dtype), (dv, "dv", (T, HV, D), q.dtype),
+                (dg, "dg", (T, HV), f32), (dbeta, "dbeta", (T, HV), f32),
+                (d_initial_state, "d_initial_state", sq, f32))
+    dt = _dtype(q)
+    nbytes = 0
+    if isinstance(workspace, str):
+        nbytes = max(int(lib.kda_gdr_chunk_bwd_workspace_bytes(N, T, HK, HV, D, dt)), 16)
+    workspace, nbytes = _workspace(workspace, nbytes, q.device)
+    _check(lib.kda_gdr_chunk_bwd_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
+                                    _ptr(initial_state), _ptr(cu_seqlens), N, T, HK, HV, D, dt,
+                                    _ptr(d_o), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv),
+                                    _ptr(dg), _ptr(dbeta), _ptr(d_initial_state), _ptr(workspace),
+                                    nbytes, _stream(stream)))
+    return dq, dk, dv, dg, dbeta, d_initial_state
+
+
+def kda_prologue_bwd_workspace_bytes(N: int, T: int, H: int, D: int, dtype: torch.dtype) -> int:
+    """Scratch bytes of :func:`kda_prologue_bwd` (may be 0)."""
+    return int(lib.kda_prologue_bwd_workspace_bytes(N, T, H, D, _DTYPES[dtype]))
+
+
+def kda_prologue_bwd(x, conv_w, dq, dk, dv, dx, d_conv_w=None, *, H: int, D: int, cache_in=None,
+                     d_cache_in=None, cu_seqlens=None, workspace="auto", stream=None):
+    """Gradients of :func:`kda_prologue` for L = sum(dq * q) + sum(dk * k) + sum(dv * v):
+    writes ``dx`` (x's dtype) and, where given, ``d_conv_w`` [3*H*D, 4] (fp32) and
+    ``d_cache_in`` (x's dtype).  ``dq, dk, dv`` [T, H, D] share a dtype of their own."""
+    T, C = x.shape[0], 3 * H * D
+    N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    f32 = torch.float32
+    _expect(x.device, (x, "x", (T, C), x.dtype), (conv_w, "conv_w", (C, 4), f32),
+            (dq, "dq", (T, H, D), dq.dtype), (dk, "dk", (T, H, D), dq.dtype),
+            (dv, "dv", (T, H, D), dq.dtype), (dx, "dx", (T, C), x.dtype),
+            (d_conv_w, "d_conv_w", (C, 4), f32), (cache_in, "cache_in", (N, 3, C), x.dtype),
+            (d_cache_in, "d_cache_in", (N, 3, C), x.dtype),
+            (cu_seqlens, "cu_seqlens", (N + 1,), torch.int32))
+    dt = _dtype(x)
+    nbytes = 0
+    if isinstance(workspace, str) and d_conv_w is not None:
+        nbytes = int(lib.kda_prologue_bwd_workspace_bytes(N, T, H, D, dt))
+    workspace, nbytes = _workspace(workspace, nbytes, x.device)
+    _check(lib.kda_prologue_bwd(_ptr(x), _ptr(conv_w), _ptr(cache_in), _ptr(cu_seqlens), N, T, H, D,
+                                dt, _dtype(dq), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dx),
+                                _ptr(d_conv_w), _ptr(d_cache_in), _ptr(workspace), nbytes,
+                                _stream(stream)))
+
+
+def kda_output_epilogue_bwd_workspace_bytes(T: int, H: int, D: int) -> int:
+    """Scratch bytes of :func:`kda_output_epilogue_bwd` (may be 0)."""
+    return int(lib.kda_output_epilogue_bwd_workspace_bytes(T, H, D))
+
+
+def kda_output_epilogue_bwd(o, gate, weight, d_out, d_o, d_gate, d_weight=None, *,
+                            eps: float = 1e-5, workspace="auto", stream=None):
+    """Gradients of :func:`kda_output_epilogue` for L = sum(d_out * out): writes ``d_o`` (fp32),
+    ``d_gate`` (gate's dtype) and, where given, ``d_weight`` [D] (fp32)."""
+    if o.dim() != 3:
+        raise ValueError("o has three dimensions: tokens, heads, channels")
+    T, H, D = o.shape
+    f32, dt = torch.float32, gate.dtype
+    _expect(o.device, (o, "o", (T, H, D), f32), (gate, "gate", (T, H, D), dt),
+            (weight, "weight", (D,), f32), (d_out, "d_out", (T, H, D), dt),
+            (d_o, "d_o", (T, H, D), f32), (d_gate, "d_gate", (T, H, D), dt),
+            (d_weight, "d_weight", (D,), f32))
+    nbytes = 0
+    if isinstance(workspace, str) and d_weight is not None:
+        nbytes = int(lib.kda_output_epilogue_bwd_workspace_bytes(T, H, D))
+    workspace, nbytes = _workspace(workspace, nbytes, o.device)
+    _check(lib.kda_output_epilogue_bwd(_ptr(o), _ptr(gate), _ptr(weight), float(eps), _ptr(d_out), T,
+                                       H, D, _dtype(gate), _ptr(d_o), _ptr(d_gate), _ptr(d_weight),
+                                       _ptr(workspace), nbytes, _stream(stream)))

@@ -12,6 +12,7 @@
 
 #include "kda_chunk_record.cuh"
 #include "kda_common.cuh"
+#include "kda_gdr.cuh"
 
 namespace {
 
@@ -937,6 +938,319 @@ kda_status kda_state_compose(const float *M, const float *B, const float *E_in, 
               "E_out overlaps an input");
   cudaError_t e = kda::launch_state_compose(M, B, E_in, E_out, N * H, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "kda_state_compose launch");
+  return KDA_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Gated delta rule with one decay per head, and the backward passes of the
+// prologue and of the output epilogue
+// ---------------------------------------------------------------------------
+
+namespace {
+
+struct Span {
+  const char *name;
+  const void *p;
+  size_t bytes;
+};
+
+// No output overlaps an input or another output (null spans are skipped).
+kda_status check_disjoint(const Span *outs, int n_out, const Span *ins, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < n_in; ++j)
+      KDA_REQUIRE(!overlaps(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes), "%s overlaps %s",
+                  outs[i].name, ins[j].name);
+    for (int j = i + 1; j < n_out; ++j)
+      KDA_REQUIRE(!overlaps(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes), "%s overlaps %s",
+                  outs[i].name, outs[j].name);
+  }
+  return KDA_OK;
+}
+
+kda_status check_gdr_sizes(int N, int T, int HK, int HV, int D, kda_dtype dt,
+                           const int32_t *cu_seqlens, const char *what, bool one_token = false) {
+  KDA_REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  KDA_REQUIRE(N >= 1 && T >= 0 && HK >= 1 && HV >= 1 && D >= 1,
+              "bad sizes N=%d T=%d HK=%d HV=%d D=%d", N, T, HK, HV, D);
+  KDA_REQUIRE(HV % HK == 0, "HV=%d is not a multiple of HK=%d", HV, HK);
+  KDA_REQUIRE(one_token || cu_seqlens != nullptr || N == 1, "cu_seqlens is NULL but N=%d", N);
+  KDA_OPT_PTR4(cu_seqlens, "cu_seqlens");
+  if (!supported_d(D)) return fail(KDA_ERR_UNSUPPORTED, "%s: D=%d not in {16,32,64,128}", what, D);
+  KDA_REQUIRE((long long)N * HV * 4 < (1LL << 31), "N*HV too large");
+  return KDA_OK;
+}
+
+bool gdr_chunk_path(int T, int D, kda_dtype dt) {
+  return (dt == KDA_BF16 || dt == KDA_F16) && (D == 64 || D == 128) && T > 0;
+}
+
+bool gdr_sizes_ok(int N, int T, int HK, int HV, int D, kda_dtype dt) {
+  return N >= 1 && T >= 0 && HK >= 1 && HV >= 1 && HV % HK == 0 && gdr_chunk_path(T, D, dt);
+}
+
+// Arguments of the forward entry points; `ws` is checked as one more output.
+kda_status check_gdr_fwd(const void *q, const void *k, const void *v, const float *g,
+                         const float *beta, const float *initial_state, const int32_t *cu_seqlens,
+                         int N, int T, int HK, int HV, int D, kda_dtype dt, float *o,
+                         float *final_state, void *ws, size_t ws_bytes, const char *what,
+                         bool one_token = false) {
+  kda_status st = check_gdr_sizes(N, T, HK, HV, D, dt, cu_seqlens, what, one_token);
+  if (st != KDA_OK) return st;
+  if (T > 0) {
+    KDA_REQUIRE_PTR(q, "q");
+    KDA_REQUIRE_PTR(k, "k");
+    KDA_REQUIRE_PTR(v, "v");
+    KDA_REQUIRE_PTR4(g, "g");
+    KDA_REQUIRE_PTR4(beta, "beta");
+    KDA_REQUIRE_PTR(o, "o");
+  }
+  KDA_OPT_PTR(initial_state, "initial_state");
+  KDA_OPT_PTR(final_state, "final_state");
+  const size_t es = esize(dt), qk = (size_t)T * HK * D * es, gb = (size_t)T * HV * 4;
+  const size_t sb = (size_t)N * HV * D * D * 4;
+  const bool in_place = final_state == initial_state;
+  const Span outs[3] = {{"o", o, (size_t)T * HV * D * 4}, {"final_state", final_state, sb},
+                        {"workspace", ws, ws_bytes}};
+  const Span ins[7] = {{"q", q, qk}, {"k", k, qk}, {"v", v, (size_t)T * HV * D * es}, {"g", g, gb},
+                       {"beta", beta, gb}, {"cu_seqlens", cu_seqlens, (size_t)(N + 1) * 4},
+                       {"initial_state", in_place ? nullptr : initial_state, sb}};
+  return check_disjoint(outs, 3, ins, 7);
+}
+
+}  // namespace
+
+extern "C" {
+
+kda_status kda_gdr_recurrent(const void *q, const void *k, const void *v, const float *g,
+                             const float *beta, float scale, const float *initial_state,
+                             const int32_t *cu_seqlens, int N, int T, int HK, int HV, int D,
+                             kda_dtype dt, float *o, float *final_state, kda_stream_t stream) {
+  kda_status st = check_gdr_fwd(q, k, v, g, beta, initial_state, cu_seqlens, N, T, HK, HV, D, dt, o,
+                                final_state, nullptr, 0, "gdr_recurrent");
+  if (st != KDA_OK) return st;
+  if (T == 0 && final_state == nullptr) return KDA_OK;
+  int *status = nullptr;
+  st = device_status_word(&status);
+  if (st != KDA_OK) return st;
+  const cudaError_t e =
+      kda::launch_gdr_recurrent(q, k, v, g, beta, scale, initial_state, cu_seqlens, false, N, T, HK,
+                                HV, D, dt, o, final_state, status, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kda_gdr_recurrent launch");
+  return KDA_OK;
+}
+
+kda_status kda_gdr_decode_step(const void *q, const void *k, const void *v, const float *g,
+                               const float *beta, float scale, float *state, int N, int HK, int HV,
+                               int D, kda_dtype dt, float *o, kda_stream_t stream) {
+  KDA_REQUIRE_PTR(state, "state");
+  kda_status st = check_gdr_fwd(q, k, v, g, beta, state, nullptr, N, N, HK, HV, D, dt, o, state,
+                                nullptr, 0, "gdr_decode_step", true);
+  if (st != KDA_OK) return st;
+  int *status = nullptr;
+  st = device_status_word(&status);
+  if (st != KDA_OK) return st;
+  const cudaError_t e =
+      kda::launch_gdr_recurrent(q, k, v, g, beta, scale, state, nullptr, true, N, N, HK, HV, D, dt,
+                                o, state, status, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kda_gdr_decode_step launch");
+  return KDA_OK;
+}
+
+size_t kda_gdr_chunk_fwd_workspace_bytes(int N, int T, int HK, int HV, int D, kda_dtype dt) {
+  return gdr_sizes_ok(N, T, HK, HV, D, dt) ? kda::gdr::layout(N, T, HK, HV, D, false).bytes : 0;
+}
+
+size_t kda_gdr_chunk_bwd_workspace_bytes(int N, int T, int HK, int HV, int D, kda_dtype dt) {
+  return gdr_sizes_ok(N, T, HK, HV, D, dt) ? kda::gdr::layout(N, T, HK, HV, D, true).bytes : 0;
+}
+
+kda_status kda_gdr_chunk_fwd_ws(const void *q, const void *k, const void *v, const float *g,
+                                const float *beta, float scale, const float *initial_state,
+                                const int32_t *cu_seqlens, int N, int T, int HK, int HV, int D,
+                                kda_dtype dt, float *o, float *final_state, void *workspace,
+                                size_t workspace_bytes, kda_stream_t stream) {
+  const size_t need = kda_gdr_chunk_fwd_workspace_bytes(N, T, HK, HV, D, dt);
+  if (workspace == nullptr || need == 0)
+    return kda_gdr_recurrent(q, k, v, g, beta, scale, initial_state, cu_seqlens, N, T, HK, HV, D,
+                             dt, o, final_state, stream);
+  kda_status st = check_gdr_fwd(q, k, v, g, beta, initial_state, cu_seqlens, N, T, HK, HV, D, dt, o,
+                                final_state, workspace, need, "gdr_chunk_fwd");
+  if (st != KDA_OK) return st;
+  KDA_OPT_PTR(workspace, "workspace");
+  KDA_REQUIRE(workspace_bytes >= need, "workspace holds %zu bytes, these sizes need %zu",
+              workspace_bytes, need);
+  int *status = nullptr;
+  st = device_status_word(&status);
+  if (st != KDA_OK) return st;
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = kda::launch_gdr_prep(q, k, g, beta, cu_seqlens, N, T, HK, HV, D, dt, workspace,
+                                       false, status, s);
+  if (e == cudaSuccess)
+    e = kda::launch_gdr_state(v, initial_state, cu_seqlens, scale, N, T, HK, HV, D, dt, workspace,
+                              false, o, final_state, status, s);
+  if (e != cudaSuccess) return cuda_fail(e, "kda_gdr_chunk_fwd_ws launch");
+  return KDA_OK;
+}
+
+kda_status kda_gdr_chunk_bwd_ws(const void *q, const void *k, const void *v, const float *g,
+                                const float *beta, float scale, const float *initial_state,
+                                const int32_t *cu_seqlens, int N, int T, int HK, int HV, int D,
+                                kda_dtype dt, const float *d_o, const float *d_final_state,
+                                void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                                float *d_initial_state, void *workspace, size_t workspace_bytes,
+                                kda_stream_t stream) {
+  kda_status st = check_gdr_sizes(N, T, HK, HV, D, dt, cu_seqlens, "gdr_chunk_bwd");
+  if (st != KDA_OK) return st;
+  if (!gdr_chunk_path(T, D, dt))
+    return fail(KDA_ERR_UNSUPPORTED,
+                "gdr_chunk_bwd: needs bf16/f16, D in {64,128} and T > 0 (got dt=%d D=%d T=%d)",
+                (int)dt, D, T);
+  KDA_REQUIRE_PTR(q, "q");
+  KDA_REQUIRE_PTR(k, "k");
+  KDA_REQUIRE_PTR(v, "v");
+  KDA_REQUIRE_PTR4(g, "g");
+  KDA_REQUIRE_PTR4(beta, "beta");
+  KDA_REQUIRE_PTR(d_o, "d_o");
+  KDA_REQUIRE_PTR(dq, "dq");
+  KDA_REQUIRE_PTR(dk, "dk");
+  KDA_REQUIRE_PTR(dv, "dv");
+  KDA_REQUIRE_PTR4(dg, "dg");
+  KDA_REQUIRE_PTR4(dbeta, "dbeta");
+  KDA_OPT_PTR(initial_state, "initial_state");
+  KDA_OPT_PTR(d_final_state, "d_final_state");
+  KDA_OPT_PTR(d_initial_state, "d_initial_state");
+  KDA_REQUIRE_PTR(workspace, "workspace");
+  const size_t need = kda::gdr::layout(N, T, HK, HV, D, true).bytes;
+  KDA_REQUIRE(workspace_bytes >= need, "workspace holds %zu bytes, these sizes need %zu",
+              workspace_bytes, need);
+  const size_t es = esize(dt), qk = (size_t)T * HK * D * es, vb = (size_t)T * HV * D * es;
+  const size_t gb = (size_t)T * HV * 4, sb = (size_t)N * HV * D * D * 4;
+  const Span outs[7] = {{"dq", dq, qk}, {"dk", dk, qk}, {"dv", dv, vb}, {"dg", dg, gb},
+                        {"dbeta", dbeta, gb}, {"d_initial_state", d_initial_state, sb},
+                        {"workspace", workspace, need}};
+  const Span ins[9] = {{"q", q, qk}, {"k", k, qk}, {"v", v, vb}, {"g", g, gb}, {"beta", beta, gb},
+                       {"d_o", d_o, (size_t)T * HV * D * 4}, {"initial_state", initial_state, sb},
+                       {"d_final_state", d_final_state, sb},
+                       {"cu_seqlens", cu_seqlens, (size_t)(N + 1) * 4}};
+  st = check_disjoint(outs, 7, ins, 9);
+  if (st != KDA_OK) return st;
+  int *status = nullptr;
+  st = device_status_word(&status);
+  if (st != KDA_OK) return st;
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = kda::launch_gdr_prep(q, k, g, beta, cu_seqlens, N, T, HK, HV, D, dt, workspace,
+                                       true, status, s);
+  if (e == cudaSuccess)
+    e = kda::launch_gdr_state(v, initial_state, cu_seqlens, scale, N, T, HK, HV, D, dt, workspace,
+                              true, nullptr, nullptr, status, s);
+  if (e == cudaSuccess)
+    e = kda::launch_gdr_bwd(v, g, beta, cu_seqlens, scale, N, T, HK, HV, D, dt, workspace, d_o,
+                            d_final_state, dq, dk, dv, dg, dbeta, d_initial_state, status, s);
+  if (e != cudaSuccess) return cuda_fail(e, "kda_gdr_chunk_bwd_ws launch");
+  return KDA_OK;
+}
+
+size_t kda_prologue_bwd_workspace_bytes(int N, int T, int H, int D, kda_dtype dt) {
+  if (N < 1 || T < 0 || H < 1 || !supported_d(D) || !valid_dtype(dt) ||
+      (long long)H * D * 3 >= (1LL << 31))
+    return 0;
+  return kda::prologue_bwd_workspace_bytes(T, H, D);
+}
+
+kda_status kda_prologue_bwd(const void *x, const float *conv_w, const void *cache_in,
+                            const int32_t *cu_seqlens, int N, int T, int H, int D, kda_dtype dt,
+                            kda_dtype grad_dt, const void *dq, const void *dk, const void *dv,
+                            void *dx, float *d_conv_w, void *d_cache_in, void *workspace,
+                            size_t workspace_bytes, kda_stream_t stream) {
+  KDA_REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  KDA_REQUIRE(valid_dtype(grad_dt), "unknown gradient dtype %d", (int)grad_dt);
+  KDA_REQUIRE(N >= 1 && T >= 0 && H >= 1 && D >= 1, "bad sizes N=%d T=%d H=%d D=%d", N, T, H, D);
+  KDA_REQUIRE(cu_seqlens != nullptr || N == 1, "cu_seqlens is NULL but N=%d", N);
+  if (!supported_d(D))
+    return fail(KDA_ERR_UNSUPPORTED, "prologue_bwd: D=%d not in {16,32,64,128}", D);
+  KDA_REQUIRE((long long)H * D * 3 < (1LL << 31), "3*H*D too large");
+  if (T > 0) {
+    KDA_REQUIRE_PTR(x, "x");
+    KDA_REQUIRE_PTR(dq, "dq");
+    KDA_REQUIRE_PTR(dk, "dk");
+    KDA_REQUIRE_PTR(dv, "dv");
+    KDA_REQUIRE_PTR(dx, "dx");
+  }
+  KDA_REQUIRE_PTR(conv_w, "conv_w");
+  KDA_OPT_PTR(cache_in, "cache_in");
+  KDA_OPT_PTR(d_conv_w, "d_conv_w");
+  KDA_OPT_PTR(d_cache_in, "d_cache_in");
+  KDA_OPT_PTR4(cu_seqlens, "cu_seqlens");
+  size_t need = kda::prologue_bwd_workspace_bytes(T, H, D);
+  if (d_conv_w == nullptr) need = 0;
+  if (need > 0) {
+    KDA_REQUIRE_PTR(workspace, "workspace");
+    KDA_REQUIRE(workspace_bytes >= need, "workspace holds %zu bytes, these sizes need %zu",
+                workspace_bytes, need);
+  }
+  const size_t Cn = (size_t)3 * H * D, es = esize(dt);
+  const size_t xb = (size_t)T * Cn * es, gr = (size_t)T * H * D * esize(grad_dt);
+  const size_t cb = (size_t)N * 3 * Cn * es;
+  const Span outs[4] = {{"dx", dx, xb}, {"d_conv_w", d_conv_w, Cn * 16},
+                        {"d_cache_in", d_cache_in, cb}, {"workspace", workspace, need}};
+  const Span ins[7] = {{"x", x, xb}, {"conv_w", conv_w, Cn * 16}, {"cache_in", cache_in, cb},
+                       {"dq", dq, gr}, {"dk", dk, gr}, {"dv", dv, gr},
+                       {"cu_seqlens", cu_seqlens, (size_t)(N + 1) * 4}};
+  kda_status st = check_disjoint(outs, 4, ins, 7);
+  if (st != KDA_OK) return st;
+  int *status = nullptr;
+  st = device_status_word(&status);
+  if (st != KDA_OK) return st;
+  const cudaError_t e =
+      kda::launch_prologue_bwd(x, conv_w, cache_in, cu_seqlens, N, T, H, D, dt, grad_dt, dq, dk, dv,
+                               dx, d_conv_w, d_cache_in, workspace, status, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kda_prologue_bwd launch");
+  return KDA_OK;
+}
+
+size_t kda_output_epilogue_bwd_workspace_bytes(int T, int H, int D) {
+  if (T < 0 || H < 1 || !supported_d(D)) return 0;
+  return kda::epilogue_bwd_workspace_bytes((long long)T * H, D);
+}
+
+kda_status kda_output_epilogue_bwd(const float *o, const void *gate, const float *weight, float eps,
+                                   const void *d_out, int T, int H, int D, kda_dtype dt, float *d_o,
+                                   void *d_gate, float *d_weight, void *workspace,
+                                   size_t workspace_bytes, kda_stream_t stream) {
+  KDA_REQUIRE(valid_dtype(dt), "unknown dtype %d", (int)dt);
+  KDA_REQUIRE(T >= 0 && H >= 1 && D >= 1, "bad sizes T=%d H=%d D=%d", T, H, D);
+  if (!supported_d(D))
+    return fail(KDA_ERR_UNSUPPORTED, "epilogue_bwd: D=%d not in {16,32,64,128}", D);
+  KDA_REQUIRE(eps >= 0.f && eps < 1e30f, "eps must be finite and non-negative");
+  KDA_REQUIRE_PTR(weight, "weight");
+  if (T > 0) {
+    KDA_REQUIRE_PTR(o, "o");
+    KDA_REQUIRE_PTR(gate, "gate");
+    KDA_REQUIRE_PTR(d_out, "d_out");
+    KDA_REQUIRE_PTR(d_o, "d_o");
+    KDA_REQUIRE_PTR(d_gate, "d_gate");
+  }
+  KDA_OPT_PTR(d_weight, "d_weight");
+  const long long rows = (long long)T * H;
+  size_t need = kda::epilogue_bwd_workspace_bytes(rows, D);
+  if (d_weight == nullptr) need = 0;
+  if (need > 0) {
+    KDA_REQUIRE_PTR(workspace, "workspace");
+    KDA_REQUIRE(workspace_bytes >= need, "workspace holds %zu bytes, these sizes need %zu",
+                workspace_bytes, need);
+  }
+  const size_t n = (size_t)rows * D, es = esize(dt);
+  const Span outs[4] = {{"d_o", d_o, n * 4}, {"d_gate", d_gate, n * es},
+                        {"d_weight", d_weight, (size_t)D * 4}, {"workspace", workspace, need}};
+  const Span ins[4] = {{"o", o, n * 4}, {"gate", gate, n * es}, {"weight", weight, (size_t)D * 4},
+                       {"d_out", d_out, n * es}};
+  kda_status st = check_disjoint(outs, 4, ins, 4);
+  if (st != KDA_OK) return st;
+  const cudaError_t e = kda::launch_epilogue_bwd(o, gate, weight, eps, d_out, rows, D, dt, d_o,
+                                                 d_gate, d_weight, workspace, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "kda_output_epilogue_bwd launch");
   return KDA_OK;
 }
 

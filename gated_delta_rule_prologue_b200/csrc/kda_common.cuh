@@ -294,6 +294,24 @@ cudaError_t launch_decode(const void *x, const float *w, void *cache, const void
                           float lower_bound, bool gated, int *status, cudaStream_t s);
 cudaError_t launch_epilogue(const float *o, const void *gate, const float *weight, float eps,
                             long long rows, int D, kda_dtype dt, void *out, cudaStream_t s);
+// Backward of the output epilogue and of the prologue; ws holds the partial sums of the
+// weights' gradients (bytes as below, 0: none needed).
+size_t epilogue_bwd_workspace_bytes(long long rows, int D);
+cudaError_t launch_epilogue_bwd(const float *o, const void *gate, const float *weight, float eps,
+                                const void *d_out, long long rows, int D, kda_dtype dt, float *d_o,
+                                void *d_gate, float *d_weight, void *ws, cudaStream_t s);
+size_t prologue_bwd_workspace_bytes(int T, int H, int D);
+cudaError_t launch_prologue_bwd(const void *x, const float *w, const void *cache_in,
+                                const int32_t *cu, int N, int T, int H, int D, kda_dtype dt,
+                                kda_dtype gdt, const void *dq, const void *dk, const void *dv,
+                                void *dx, float *dw, void *d_cache, void *ws, int *status,
+                                cudaStream_t s);
+// Gated delta rule with one decay per head, token by token; one_token: sequence n is token n.
+cudaError_t launch_gdr_recurrent(const void *q, const void *k, const void *v, const float *g,
+                                 const float *beta, float scale, const float *s0,
+                                 const int32_t *cu, bool one_token, int N, int T, int HK, int HV,
+                                 int D, kda_dtype dt, float *o, float *sN, int *status,
+                                 cudaStream_t s);
 cudaError_t launch_chunk_simt(const void *q, const void *k, const void *v, const float *g,
                               const float *beta, float scale, const float *s0,
                               const int32_t *cu, int N, int T, int H, int D, int chunk,

@@ -1,0 +1,237 @@
+// Chunked gated delta rule with one decay per head and token: shared parts of the prep pass
+// (kda_gdr_prep.cu), the state pass (kda_gdr_state.cu) and the backward (kda_gdr_bwd.cu).
+//
+// Mathematics, per value head with key head h / (HV / HK), chunks of C = 64 tokens, entry state
+// S (D x D, key-first), gamma_r the inclusive sum of g inside the chunk, G_r = exp(gamma_r),
+// D_ri = exp(gamma_r - gamma_i) for i <= r, E_r = exp(gamma_C - gamma_r):
+//     A  = strictly lower (beta_r D_ri k_r.k_i),   T = (I + A)^-1,   P = lower (D_ri q_r.k_i)
+//     U  = T (beta (V - G K S)),   O = scale (G Q S + P U),   S' = G_C S + K^T (E U)
+// Every decay factor is exp of a difference that is never positive when g is not, so no factor
+// leaves the fp32 range, whatever the decay; gamma is summed in fp64, so a token that all but
+// erases the state (g down to -256, where exp is 0 in fp32; smaller g counts as -256) leaves the
+// differences behind it exact.
+//
+// Arithmetic.  Products run on the tensor cores with fp32 sums.  The keys and queries are exact
+// in fp16 (one power of two per 64-token tile keeps bf16 inputs of any size in range); every
+// other operand (state, U, T, P, gradients) is split in two fp16 terms, x 2^-e = hi + lo, with a
+// power of two per row that puts the row's largest value in [1, 2): 22 significant bits, so
+// results carry fp32-like errors and no value of the fp32 range overflows.  A product of a split
+// operand with an exact one takes two MMAs, of two split ones three (hi hi, hi lo, lo hi).
+//
+// Workspace: records of the chunks.  Chunk c of sequence n, whose first token is bos, has slot
+// bos / 64 + n + c (strictly increasing from chunk to chunk, so no index pass is needed; T / 64 +
+// N + 1 slots).
+//   KQ record (slot, key head):   K tile, Q tile: 64 rows x D fp16, 64-column blocks of 64 rows x
+//                                 128 bytes with the 16-byte pieces XOR-swizzled by the row;
+//                                 {2^eK, 2^eQ} as two floats
+//   TP record (slot, value head): T hi, T lo, P hi, P lo: 64 x 64 fp16 tiles, same layout, rows
+//                                 scaled; then fp32 [64]: G, E, 2^eT, 2^eP, beta
+#pragma once
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace gdr {
+
+constexpr int C = 64;
+
+// Tile layout: byte offset of the 16-byte piece c8 (columns 8 c8 ..) of a row of a tile of R rows.
+template <int R = C> __host__ __device__ constexpr uint32_t tile_off(int row, int c8) {
+  return (uint32_t)((c8 >> 3) * (R * 128) + row * 128 + (((c8 & 7) ^ (row & 7)) << 4));
+}
+
+constexpr uint32_t kTriBytes = C * C * 2;  // one 64 x 64 fp16 tile
+constexpr uint32_t kT_HI = 0, kT_LO = kTriBytes, kP_HI = 2 * kTriBytes, kP_LO = 3 * kTriBytes;
+constexpr uint32_t kVec = 4 * kTriBytes;
+enum { kVecG = 0, kVecE = 1, kVecT = 2, kVecP = 3, kVecBeta = 4, kVecs = 5 };
+constexpr uint32_t kTpBytes = kVec + kVecs * C * 4;
+__host__ __device__ constexpr uint32_t kq_tile_bytes(int D) { return (uint32_t)C * D * 2; }
+__host__ __device__ constexpr uint32_t kq_bytes(int D) { return 2 * kq_tile_bytes(D) + 128; }
+
+__host__ __device__ inline long long slots(int N, int T) { return (long long)T / C + N + 1; }
+__host__ __device__ inline long long first_slot(int bos, int n) { return bos / C + n; }
+
+// Byte offsets in the workspace.
+struct Layout {
+  size_t kq, tp;                 // records
+  size_t state, dstate, u, x;    // backward: per chunk fp32 S and dS' [D][D] (value-major), U and X [64][D]
+  size_t bytes;
+};
+__host__ __device__ inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
+  const size_t n = (size_t)slots(N, T);
+  Layout l;
+  l.kq = 0;
+  l.tp = l.kq + n * HK * kq_bytes(D);
+  l.state = l.tp + n * HV * kTpBytes;
+  const size_t sq = n * HV * (size_t)D * D * 4, rows = n * HV * (size_t)C * D * 4;
+  l.dstate = l.state + (bwd ? sq : 0);
+  l.u = l.dstate + (bwd ? sq : 0);
+  l.x = l.u + (bwd ? rows : 0);
+  l.bytes = l.x + (bwd ? rows : 0);
+  return l;
+}
+
+// The log-decay as the chunked form takes it (NaN stays NaN).
+__device__ __forceinline__ float floor_g(float g) { return g < -256.f ? -256.f : g; }
+
+// Sequence and chunk of a slot; false for a slot that no chunk has.
+__device__ __forceinline__ bool chunk_of_slot(const int32_t *cu, int N, int T, long long slot,
+                                              int *status, int &n, int &bos, int &eos, int &c) {
+  int lo = 0, hi = N - 1;
+  n = 0;
+  if (cu) {
+    while (lo <= hi) {
+      const int mid = (lo + hi) >> 1;
+      if (first_slot(cu[mid], mid) <= slot) {
+        n = mid;
+        lo = mid + 1;
+      } else {
+        hi = mid - 1;
+      }
+    }
+  }
+  seq_bounds(cu, n, T, status, bos, eos);
+  const long long cc = slot - first_slot(bos, n);
+  if (cc < 0 || cc * C >= eos - bos) return false;
+  c = (int)cc;
+  return true;
+}
+
+// ---------------------------------------------------------------------------
+// Warp-level pieces
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// 16 bytes global -> shared, zeros when !ok (nothing is read then).
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok = true) {
+  const int n = ok ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// `bytes` (a multiple of 16) by all threads of the block.
+__device__ __forceinline__ void cp_block(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+  for (uint32_t i = threadIdx.x * 16; i < bytes; i += blockDim.x * 16) cp16(dst + i, src + i);
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// c += a b: a 16 x 16 (rows lane/4, +8), b 16 x 8, fp16 operands, fp32 sums.
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two 8-column blocks (n0 .. n0 + 15) of a B operand for the 16 k-values from k0 on.
+// Rows of the tile are B's columns (n), 16-byte pieces its k: r = {b0, b1, b0', b1'}.
+__device__ __forceinline__ void load_b(uint32_t (&r)[4], uint32_t tile, int n0, int k0) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4(r, tile + tile_off(n0 + (m >> 1) * 8 + (lane & 7), (k0 >> 3) + (m & 1)));
+}
+// Rows of the tile are B's k.
+template <int R = C> __device__ __forceinline__ void load_bt(uint32_t (&r)[4], uint32_t tile, int n0, int k0) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4t(r, tile + tile_off<R>(k0 + (m & 1) * 8 + (lane & 7), (n0 >> 3) + (m >> 1)));
+}
+// A operand (16 rows from m0, 16 k from k0): rows of the tile are A's rows.
+__device__ __forceinline__ void load_a(uint32_t (&r)[4], uint32_t tile, int m0, int k0) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4(r, tile + tile_off(m0 + (m & 1) * 8 + (lane & 7), (k0 >> 3) + (m >> 1)));
+}
+// Rows of the tile are A's k (the transposed tile is the operand).
+__device__ __forceinline__ void load_at(uint32_t (&r)[4], uint32_t tile, int m0, int k0) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4t(r, tile + tile_off(k0 + (m >> 1) * 8 + (lane & 7), (m0 >> 3) + (m & 1)));
+}
+
+// Power of two s with x / s in [1, 2) for x = the largest magnitude of a row (any s for 0), and
+// its inverse.  Exponents are kept in the range where both are normal numbers.
+struct Scale {
+  float s, inv;
+};
+__device__ __forceinline__ Scale scale_of(float largest) {
+  int e = (int)(__float_as_uint(largest) >> 23) & 255;
+  e = min(max(e, 1), 253);
+  return {__uint_as_float((uint32_t)e << 23), __uint_as_float((uint32_t)(254 - e) << 23)};
+}
+// The largest of the four lanes that share accumulator rows.
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  return x + __shfl_xor_sync(0xffffffffu, x, 2);
+}
+
+// (x, y) inv = hi + lo, each term rounded to fp16 (nearest): the first keeps 11 bits, the second
+// the next 11, so the pair is off by at most 2^-23 of the value (2^-25 absolute near zero).
+__device__ __forceinline__ void split2(float x, float y, float inv, uint32_t &hi, uint32_t &lo) {
+  const float2 v = __fmul2_rn(make_float2(x, y), make_float2(inv, inv));
+  const __half2 h = __floats2half2_rn(v.x, v.y);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(v.x - f.x, v.y - f.y);
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// Row scales of an accumulator of NT 8-column blocks (rows lane/4 and lane/4 + 8).
+template <int NT> __device__ __forceinline__ void row_scales(const float (&c)[NT][4], Scale &r0, Scale &r1) {
+  float a = 0.f, b = 0.f;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    a = fmaxf(a, fmaxf(fabsf(c[i][0]), fabsf(c[i][1])));
+    b = fmaxf(b, fmaxf(fabsf(c[i][2]), fabsf(c[i][3])));
+  }
+  r0 = scale_of(quad_max(a));
+  r1 = scale_of(quad_max(b));
+}
+// The A operand of k-step kk (columns 16 kk ..) from an accumulator, as two fp16 terms.
+template <int NT>
+__device__ __forceinline__ void split_a(const float (&c)[NT][4], int kk, const Scale &r0, const Scale &r1,
+                                        uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+  split2(c[2 * kk][0], c[2 * kk][1], r0.inv, hi[0], lo[0]);
+  split2(c[2 * kk][2], c[2 * kk][3], r1.inv, hi[1], lo[1]);
+  split2(c[2 * kk + 1][0], c[2 * kk + 1][1], r0.inv, hi[2], lo[2]);
+  split2(c[2 * kk + 1][2], c[2 * kk + 1][3], r1.inv, hi[3], lo[3]);
+}
+
+template <int NT> __device__ __forceinline__ void zero(float (&c)[NT][4]) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+}
+
+}  // namespace gdr
+
+// Host side (kda_gdr_*.cu), called by kda_api.cu.
+cudaError_t launch_gdr_prep(const void *q, const void *k, const float *g, const float *beta,
+                            const int32_t *cu, int N, int T, int HK, int HV, int D, kda_dtype dt,
+                            void *ws, bool bwd, int *status, cudaStream_t s);
+cudaError_t launch_gdr_state(const void *v, const float *s0, const int32_t *cu, float scale, int N,
+                             int T, int HK, int HV, int D, kda_dtype dt, void *ws, bool bwd, float *o,
+                             float *sN, int *status, cudaStream_t s);
+cudaError_t launch_gdr_bwd(const void *v, const float *g, const float *beta, const int32_t *cu,
+                           float scale, int N, int T, int HK, int HV, int D, kda_dtype dt, void *ws,
+                           const float *d_o, const float *d_sN, void *dq, void *dk, void *dv,
+                           float *dg, float *dbeta, float *d_s0, int *status, cudaStream_t s);
+}  // namespace kda

@@ -1,0 +1,335 @@
+// State pass of the chunked gated delta rule (kda_gdr.cuh): the chunks of a sequence in order.
+//
+// The rows of S^T (one per value channel) need nothing from one another, so a warp owns 16 of
+// them as the accumulators of its MMAs and carries them through all chunks of its (sequence,
+// value head) without a word to another warp.  Everything is computed transposed, with the value
+// channels as the MMAs' rows, because an accumulator of one product is then, split in two fp16
+// terms in registers, the A operand of the next:
+//     (K S)^T = S^T K^T            B: the K tile, read along its rows
+//     (Q S)^T = S^T Q^T
+//     R^T = beta (V^T - G (K S)^T)
+//     U^T = R^T T^T                B: the T tiles (blocks above the diagonal skipped)
+//     O^T = scale (G (Q S)^T + U^T P^T)
+//     S^T = G_C S^T + (E U)^T K    B: the K tile, read across (ldmatrix.trans)
+// The records and the V tile of the next chunk arrive by cp.async while this one is computed;
+// the CTA's two barriers per chunk only guard the two buffers.
+//
+// D = 128: 504 MMAs (16 x 8 x 16) per warp and chunk.  mma.sync runs at 9 cycles per MMA and SM
+// quarter (527 TFLOP/s measured over the GPU); with eight warps (a whole head) per CTA that is
+// what bounds the pass when there are chains enough, and with fewer chains than SMs a chain's
+// latency does.  Then a head is split over two CTAs of four warps, one per SM quarter.
+#include "kda_gdr.cuh"
+
+namespace kda {
+namespace {
+using namespace gdr;
+
+template <int D, int NW> struct StateSmem {
+  static constexpr uint32_t kK = 0, kQ = kq_tile_bytes(D);
+  static constexpr uint32_t kScales = 2 * kq_tile_bytes(D);
+  static constexpr uint32_t kTp = kq_bytes(D);
+  static constexpr uint32_t kV = kTp + kTpBytes;               // [64][16 NW] 16-bit, swizzled
+  static constexpr uint32_t kStage = kV + C * 32 * NW;
+  static constexpr uint32_t kBytes = 2 * kStage;
+};
+
+// Byte offset of the 16-byte piece p of token row `row` of a V tile 16 NW channels wide.
+template <int NW> __device__ __forceinline__ uint32_t v_off(int row, int p) {
+  return (uint32_t)(row * (32 * NW) + ((p ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ float2 widen2(uint32_t u, __nv_bfloat16) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ float2 widen2(uint32_t u, __half) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// kKeep: the backward's forward: S at the start of every chunk and U go to the workspace, and
+// there is no read-out.
+template <typename Tin, int D, int NW, bool kKeep>
+__global__ void __launch_bounds__(NW * 32, 1)
+gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__restrict__ cu,
+                 float scale, int N, int T, int HK, int HV, uint8_t *__restrict__ ws, Layout lay,
+                 float *__restrict__ o, float *sN, int *status) {
+  using Sm = StateSmem<D, NW>;
+  constexpr int NT = D / 8, KK = D / 16;
+  constexpr int kParts = D / (16 * NW);  // CTAs per head
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sbase = smem_addr(smem);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = blockIdx.x % kParts, nh = blockIdx.x / kParts;
+  const int n = nh / HV, h = nh % HV, hk = h / (HV / HK);
+  int bos, eos;
+  seq_bounds(cu, n, T, status, bos, eos);
+  const int chunks = (eos - bos + C - 1) / C;
+  const long long slot0 = first_slot(bos, n);
+  if (!in_range(status, slot0 + chunks, slots(N, T) + 1)) return;
+  const int ch0 = (part * NW + warp) * 16;     // the warp's first value channel
+  const int row = ch0 + lane / 4;              // and this lane's rows: row, row + 8
+  const int col = 2 * (lane & 3);
+
+  auto load = [&](int c) {
+    const uint32_t st = sbase + (c & 1) * Sm::kStage;
+    const long long slot = slot0 + c;
+    cp_block(st, ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D), kq_bytes(D));
+    cp_block(st + Sm::kTp, ws + lay.tp + (size_t)(slot * HV + h) * kTpBytes, kTpBytes);
+    constexpr int kPieces = 2 * NW;
+    const int t0 = bos + c * C, len = min(C, eos - t0);
+    for (int i = threadIdx.x; i < C * kPieces; i += NW * 32) {
+      const int r = i / kPieces, p = i % kPieces;
+      cp16(st + Sm::kV + v_off<NW>(r, p),
+           v + ((size_t)(t0 + min(r, len - 1)) * HV + h) * D + part * NW * 16 + p * 8, r < len);
+    }
+  };
+  if (chunks > 0) load(0);
+  cp_commit();
+
+  float s[NT][4];
+  zero(s);
+  if (s0) {
+    const float *p = s0 + ((size_t)nh * D + row) * D + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float2 a = *reinterpret_cast<const float2 *>(p + 8 * i);
+      const float2 b = *reinterpret_cast<const float2 *>(p + 8 * D + 8 * i);
+      s[i][0] = a.x; s[i][1] = a.y; s[i][2] = b.x; s[i][3] = b.y;
+    }
+  }
+
+  for (int c = 0; c < chunks; ++c) {
+    if (c + 1 < chunks) load(c + 1);
+    cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    const uint32_t st = sbase + (c & 1) * Sm::kStage;
+    const uint8_t *stp = smem + (c & 1) * Sm::kStage;
+    const float2 kqs = *reinterpret_cast<const float2 *>(stp + Sm::kScales);
+    const float *vec = reinterpret_cast<const float *>(stp + Sm::kTp + kVec);
+    const int t0 = bos + c * C, len = min(C, eos - t0);
+
+    if constexpr (kKeep) {
+      float *p = reinterpret_cast<float *>(ws + lay.state) +
+                 (((size_t)(slot0 + c) * HV + h) * D + row) * D + col;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
+        *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
+      }
+    }
+
+    // (K S)^T and (Q S)^T.
+    float ks[8][4], qs[8][4];
+    zero(ks);
+    zero(qs);
+    Scale a0, a1;
+    row_scales(s, a0, a1);
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      uint32_t hi[4], lo[4];
+      split_a(s, kk, a0, a1, hi, lo);
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t b[4];
+        load_b(b, st + Sm::kK, 16 * np, 16 * kk);
+        mma(ks[2 * np], hi, b[0], b[1]);
+        mma(ks[2 * np + 1], hi, b[2], b[3]);
+        mma(ks[2 * np], lo, b[0], b[1]);
+        mma(ks[2 * np + 1], lo, b[2], b[3]);
+        if constexpr (!kKeep) {
+          load_b(b, st + Sm::kQ, 16 * np, 16 * kk);
+          mma(qs[2 * np], hi, b[0], b[1]);
+          mma(qs[2 * np + 1], hi, b[2], b[3]);
+          mma(qs[2 * np], lo, b[0], b[1]);
+          mma(qs[2 * np + 1], lo, b[2], b[3]);
+        }
+      }
+    }
+    // R^T = beta (V^T - G (K S)^T), in ks.
+    {
+      const float f0 = a0.s * kqs.x, f1 = a1.s * kqs.x;
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t b[4];
+        const int m = lane >> 3, r = 16 * np + (m >> 1) * 8 + (lane & 7);
+        ldsm4t(b, st + Sm::kV + v_off<NW>(r, 2 * warp + (m & 1)));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // 8-token blocks 2 np + e
+          const int i = 2 * np + e;
+          const float2 g = *reinterpret_cast<const float2 *>(vec + kVecG * C + 8 * i + col);
+          const float2 bt = *reinterpret_cast<const float2 *>(vec + kVecBeta * C + 8 * i + col);
+          const float2 v0 = widen2(b[2 * e], Tin{}), v1 = widen2(b[2 * e + 1], Tin{});
+          ks[i][0] = bt.x * (v0.x - g.x * (f0 * ks[i][0]));
+          ks[i][1] = bt.y * (v0.y - g.y * (f0 * ks[i][1]));
+          ks[i][2] = bt.x * (v1.x - g.x * (f1 * ks[i][2]));
+          ks[i][3] = bt.y * (v1.y - g.y * (f1 * ks[i][3]));
+        }
+      }
+    }
+    // U^T = R^T T^T.
+    float u[8][4];
+    zero(u);
+    Scale r0, r1;
+    row_scales(ks, r0, r1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t hi[4], lo[4];
+      split_a(ks, kk, r0, r1, hi, lo);
+#pragma unroll
+      for (int np = kk; np < 4; ++np) {
+        uint32_t b[4], bl[4];
+        load_b(b, st + Sm::kTp + kT_HI, 16 * np, 16 * kk);
+        load_b(bl, st + Sm::kTp + kT_LO, 16 * np, 16 * kk);
+        mma(u[2 * np], hi, b[0], b[1]);
+        mma(u[2 * np + 1], hi, b[2], b[3]);
+        mma(u[2 * np], lo, b[0], b[1]);
+        mma(u[2 * np + 1], lo, b[2], b[3]);
+        mma(u[2 * np], hi, bl[0], bl[1]);
+        mma(u[2 * np + 1], hi, bl[2], bl[3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 t = *reinterpret_cast<const float2 *>(vec + kVecT * C + 8 * i + col);
+      u[i][0] *= r0.s * t.x;
+      u[i][1] *= r0.s * t.y;
+      u[i][2] *= r1.s * t.x;
+      u[i][3] *= r1.s * t.y;
+    }
+    if constexpr (kKeep) {
+      float *p = reinterpret_cast<float *>(ws + lay.u) + ((size_t)(slot0 + c) * HV + h) * C * D + row;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[(8 * i + col + (e & 1)) * D + 8 * (e >> 1)] = u[i][e];
+    } else {
+      // O^T = scale (G (Q S)^T + U^T P^T).
+      float pu[8][4];
+      zero(pu);
+      row_scales(u, r0, r1);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        uint32_t hi[4], lo[4];
+        split_a(u, kk, r0, r1, hi, lo);
+#pragma unroll
+        for (int np = kk; np < 4; ++np) {
+          uint32_t b[4], bl[4];
+          load_b(b, st + Sm::kTp + kP_HI, 16 * np, 16 * kk);
+          load_b(bl, st + Sm::kTp + kP_LO, 16 * np, 16 * kk);
+          mma(pu[2 * np], hi, b[0], b[1]);
+          mma(pu[2 * np + 1], hi, b[2], b[3]);
+          mma(pu[2 * np], lo, b[0], b[1]);
+          mma(pu[2 * np + 1], lo, b[2], b[3]);
+          mma(pu[2 * np], hi, bl[0], bl[1]);
+          mma(pu[2 * np + 1], hi, bl[2], bl[3]);
+        }
+      }
+      float *op = o + ((size_t)t0 * HV + h) * D + row;
+      const float q0 = a0.s * kqs.y, q1 = a1.s * kqs.y;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 g = *reinterpret_cast<const float2 *>(vec + kVecG * C + 8 * i + col);
+        const float2 p = *reinterpret_cast<const float2 *>(vec + kVecP * C + 8 * i + col);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 8 * i + col + (e & 1);
+          const float gg = e & 1 ? g.y : g.x, pp = e & 1 ? p.y : p.x;
+          const float x = gg * ((e >> 1 ? q1 : q0) * qs[i][e]) + (e >> 1 ? r1.s : r0.s) * pp * pu[i][e];
+          if (t < len) __stcs(op + (size_t)t * HV * D + 8 * (e >> 1), scale * x);
+        }
+      }
+    }
+    // S^T = G_C S^T + (E U)^T K.
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 e = *reinterpret_cast<const float2 *>(vec + kVecE * C + 8 * i + col);
+      u[i][0] *= e.x;
+      u[i][1] *= e.y;
+      u[i][2] *= e.x;
+      u[i][3] *= e.y;
+    }
+    row_scales(u, r0, r1);
+    uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) split_a(u, kk, r0, r1, hi[kk], lo[kk]);
+    const float gl = vec[kVecG * C + C - 1];
+    const float w0 = r0.s * kqs.x, w1 = r1.s * kqs.x;
+#pragma unroll
+    for (int j = 0; j < NT / 4; ++j) {
+      float acc[4][4];
+      zero(acc);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int np = 0; np < 2; ++np) {
+          uint32_t b[4];
+          load_bt(b, st + Sm::kK, 32 * j + 16 * np, 16 * kk);
+          mma(acc[2 * np], hi[kk], b[0], b[1]);
+          mma(acc[2 * np + 1], hi[kk], b[2], b[3]);
+          mma(acc[2 * np], lo[kk], b[0], b[1]);
+          mma(acc[2 * np + 1], lo[kk], b[2], b[3]);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float(&x)[4] = s[4 * j + i];
+        x[0] = fmaf(gl, x[0], w0 * acc[i][0]);
+        x[1] = fmaf(gl, x[1], w0 * acc[i][1]);
+        x[2] = fmaf(gl, x[2], w1 * acc[i][2]);
+        x[3] = fmaf(gl, x[3], w1 * acc[i][3]);
+      }
+    }
+    __syncthreads();  // the other buffer is free for the chunk after next
+  }
+  cp_wait<0>();
+
+  if (sN) {
+    float *p = sN + ((size_t)nh * D + row) * D + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
+      *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
+    }
+  }
+}
+
+template <typename Tin, int D, int NW, bool kKeep>
+cudaError_t launch_nw(const void *v, const float *s0, const int32_t *cu, float scale, int N, int T,
+                      int HK, int HV, void *ws, float *o, float *sN, int *status, cudaStream_t s) {
+  auto kern = gdr_state_kernel<Tin, D, NW, kKeep>;
+  const int bytes = (int)StateSmem<D, NW>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const long long ctas = (long long)N * HV * (D / (16 * NW));
+  if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
+  kern<<<(unsigned)ctas, NW * 32, bytes, s>>>(static_cast<const Tin *>(v), s0, cu, scale, N, T, HK,
+                                              HV, static_cast<uint8_t *>(ws),
+                                              layout(N, T, HK, HV, D, kKeep), o, sN, status);
+  return cudaGetLastError();
+}
+
+template <typename Tin, bool kKeep>
+cudaError_t launch_d(int D, const void *v, const float *s0, const int32_t *cu, float scale, int N,
+                     int T, int HK, int HV, void *ws, float *o, float *sN, int *status,
+                     cudaStream_t s) {
+  if (D == 64)
+    return launch_nw<Tin, 64, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
+  if (D != 128) return cudaErrorInvalidValue;
+  // Two CTAs per head as long as they all run at once (one per SM).
+  if ((long long)N * HV * 2 <= 148)
+    return launch_nw<Tin, 128, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
+  return launch_nw<Tin, 128, 8, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
+}
+
+}  // namespace
+
+cudaError_t launch_gdr_state(const void *v, const float *s0, const int32_t *cu, float scale, int N,
+                             int T, int HK, int HV, int D, kda_dtype dt, void *ws, bool bwd, float *o,
+                             float *sN, int *status, cudaStream_t s) {
+  if (dt == KDA_BF16)
+    return bwd ? launch_d<__nv_bfloat16, true>(D, v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s)
+               : launch_d<__nv_bfloat16, false>(D, v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
+  return bwd ? launch_d<__half, true>(D, v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s)
+             : launch_d<__half, false>(D, v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
+}
+
+}  // namespace kda

@@ -533,6 +533,135 @@ kda_status kda_output_epilogue(const float *o, const void *gate, const float *we
                                kda_stream_t stream);
 
 /*
+ * Gated delta rule with one decay per head and token.  The recurrence of this
+ * header with alpha_t = exp(g_t) a scalar per value head (the head-wise gate
+ * that [W5 §4] and [W3 "KDA 谱系速查"] place before KDA's per-channel one), and
+ * with keys and queries shared by groups of value heads:
+ *     S <- exp(g_t) S;  e <- v_t - S^T k_t;  S <- S + beta_t k_t e^T;
+ *     o_t <- scale * S^T q_t
+ * Common arguments of the kda_gdr_* entry points:
+ *   q, k          [T, HK, D] dt, unit-normalised like kda_prologue's (the
+ *                 recurrence is computed for any k; with norms above 1 it may
+ *                 grow without bound).  Value head h uses key head h / (HV / HK)
+ *   v             [T, HV, D] dt
+ *   g             [T, HV] f32, g <= 0 (4-byte aligned).  The chunked forms take
+ *                 g below -256 as -256 (exp is 0 in f32 either way)
+ *   beta          [T, HV] f32 (4-byte aligned)
+ *   scale         multiplier on every read
+ *   initial_state [N, HV, D, D] f32 (value-major like every state here) or NULL
+ *                 (zero)
+ *   cu_seqlens    [N+1] int32 device or NULL (N must be 1); lengths from zero on
+ *   o             [T, HV, D] f32 output; rows of tokens outside every sequence
+ *                 are not written
+ *   final_state   [N, HV, D, D] f32 output or NULL; may be initial_state itself
+ * HV must be a multiple of HK (else KDA_ERR_INVALID_ARG); D in {16, 32, 64, 128}
+ * (else KDA_ERR_UNSUPPORTED).  Outputs must not overlap inputs, workspaces or one
+ * another except as stated.  Results do not depend on what else runs: equal calls
+ * give equal bits.
+ */
+
+/*
+ * kda_gdr_recurrent -- token by token, each head's state held on chip from a
+ * sequence's first token to its last: the form for a few tokens per sequence
+ * (generation, drafted tokens), exact fp32 arithmetic for every dt.
+ */
+kda_status kda_gdr_recurrent(const void *q, const void *k, const void *v, const float *g,
+                             const float *beta, float scale, const float *initial_state,
+                             const int32_t *cu_seqlens, int N, int T, int HK, int HV, int D,
+                             kda_dtype dt, float *o, float *final_state, kda_stream_t stream);
+
+/*
+ * kda_gdr_decode_step -- one new token for each of N sequences (q, k [N, HK, D],
+ * v [N, HV, D], g, beta [N, HV], o [N, HV, D]); state [N, HV, D, D] f32 in/out.
+ */
+kda_status kda_gdr_decode_step(const void *q, const void *k, const void *v, const float *g,
+                               const float *beta, float scale, float *state, int N, int HK, int HV,
+                               int D, kda_dtype dt, float *o, kda_stream_t stream);
+
+/*
+ * kda_gdr_chunk_fwd_ws -- the prefill in chunks of 64 tokens: a prep pass over all
+ * chunks (decay matrix, Gram products, the inverse of the unit lower triangular
+ * system), then a state pass over the chunks of each sequence in order.
+ *   workspace        >= kda_gdr_chunk_fwd_workspace_bytes(...) bytes, 16-byte
+ *                    aligned, caller-owned; contents on entry do not matter.  Calls
+ *                    that may run at the same time must not share one.  NULL runs
+ *                    kda_gdr_recurrent.
+ * The chunked form is for dt KDA_BF16 or KDA_F16 and D 64 or 128; for other types
+ * and sizes (kda_gdr_chunk_fwd_workspace_bytes is 0 then) the call is
+ * kda_gdr_recurrent.  Products run on the tensor cores on fp16 terms: q and k
+ * exactly (bf16 values below 2^-14 of a 64-token tile's largest are off by up to
+ * 2^-25 of it), every other operand as two terms of 11 bits each, so errors are
+ * those of fp32 arithmetic relative to the largest values of a state row.
+ */
+size_t kda_gdr_chunk_fwd_workspace_bytes(int N, int T, int HK, int HV, int D, kda_dtype dt);
+kda_status kda_gdr_chunk_fwd_ws(const void *q, const void *k, const void *v, const float *g,
+                                const float *beta, float scale, const float *initial_state,
+                                const int32_t *cu_seqlens, int N, int T, int HK, int HV, int D,
+                                kda_dtype dt, float *o, float *final_state, void *workspace,
+                                size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_gdr_chunk_bwd_ws -- gradients of L = sum(d_o * o) + sum(d_final_state *
+ * final_state) for the o and final_state of kda_gdr_chunk_fwd_ws on the same
+ * inputs; the forward is recomputed inside the call.
+ *   d_o              [T, HV, D] f32, 16-byte aligned
+ *   d_final_state    [N, HV, D, D] f32 or NULL (zero)
+ *   dq, dk, dv       outputs of q's, k's and v's shape and type; dq and dk are sums
+ *                    over the value heads of a key head, rounded once
+ *   dg, dbeta        [T, HV] f32 outputs (4-byte aligned)
+ *   d_initial_state  [N, HV, D, D] f32 output or NULL (not written)
+ *   workspace        >= kda_gdr_chunk_bwd_workspace_bytes(...) bytes, 16-byte
+ *                    aligned, caller-owned, not NULL
+ * Supported: dt KDA_BF16 or KDA_F16, D 64 or 128, T > 0, else KDA_ERR_UNSUPPORTED.
+ * Rows of tokens outside every sequence are not written.
+ */
+size_t kda_gdr_chunk_bwd_workspace_bytes(int N, int T, int HK, int HV, int D, kda_dtype dt);
+kda_status kda_gdr_chunk_bwd_ws(const void *q, const void *k, const void *v, const float *g,
+                                const float *beta, float scale, const float *initial_state,
+                                const int32_t *cu_seqlens, int N, int T, int HK, int HV, int D,
+                                kda_dtype dt, const float *d_o, const float *d_final_state,
+                                void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                                float *d_initial_state, void *workspace, size_t workspace_bytes,
+                                kda_stream_t stream);
+
+/*
+ * kda_prologue_bwd -- gradients of L = sum(dq * q) + sum(dk * k) + sum(dv * v) for
+ * the outputs of kda_prologue on the same x, conv_w, cache_in and cu_seqlens
+ * (cache_out is taken as a constant).
+ *   dq, dk, dv   [T, H, D] grad_dt
+ *   dx           [T, 3*H*D] dt output
+ *   d_conv_w     [3*H*D, 4] f32 output or NULL (not computed)
+ *   d_cache_in   [N, 3, 3*H*D] dt output or NULL
+ *   workspace    >= kda_prologue_bwd_workspace_bytes(...) bytes, 16-byte aligned,
+ *                caller-owned; may be NULL when that is 0 or d_conv_w is NULL
+ * Supported: D in {16, 32, 64, 128}, any dt and grad_dt.  T == 0 writes zeros.
+ */
+size_t kda_prologue_bwd_workspace_bytes(int N, int T, int H, int D, kda_dtype dt);
+kda_status kda_prologue_bwd(const void *x, const float *conv_w, const void *cache_in,
+                            const int32_t *cu_seqlens, int N, int T, int H, int D, kda_dtype dt,
+                            kda_dtype grad_dt, const void *dq, const void *dk, const void *dv,
+                            void *dx, float *d_conv_w, void *d_cache_in, void *workspace,
+                            size_t workspace_bytes, kda_stream_t stream);
+
+/*
+ * kda_output_epilogue_bwd -- gradients of L = sum(d_out * out) for the out of
+ * kda_output_epilogue on the same o, gate, weight and eps.  A row of zeros has
+ * finite gradients for eps > 0 only, as it has a finite output.
+ *   d_out     [T, H, D] dt
+ *   d_o       [T, H, D] f32 output (the d_o of kda_chunk_bwd_ws and
+ *             kda_gdr_chunk_bwd_ws);  d_gate [T, H, D] dt output
+ *   d_weight  [D] f32 output or NULL (not computed)
+ *   workspace >= kda_output_epilogue_bwd_workspace_bytes(...) bytes, 16-byte
+ *             aligned, caller-owned; may be NULL when that is 0 or d_weight is NULL
+ * Supported: D in {16, 32, 64, 128}.
+ */
+size_t kda_output_epilogue_bwd_workspace_bytes(int T, int H, int D);
+kda_status kda_output_epilogue_bwd(const float *o, const void *gate, const float *weight, float eps,
+                                   const void *d_out, int T, int H, int D, kda_dtype dt, float *d_o,
+                                   void *d_gate, float *d_weight, void *workspace,
+                                   size_t workspace_bytes, kda_stream_t stream);
+
+/*
  * kda_get_device_status -- read and clear the current device's status word
  * (KDA_OK if no kernel recorded a fault).  Synchronises the device.
  */
