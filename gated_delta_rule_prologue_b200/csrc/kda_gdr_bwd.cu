@@ -626,10 +626,10 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
         sm.tail[half][r0] = d0;
         sm.tail[half][r1] = d1;
       }
-      rg0 -= d0;
-      rg1 -= d1;
     }
-    // W, M and their sums over rows and columns; Q K^T and K K^T again, from the tiles.
+    // W, M and their sums over rows and columns; Q K^T and K K^T again, from the tiles.  A token's
+    // own term decays by nothing: it stays out of the sums, where it would be added and taken
+    // away again, next to which the others may be small.
     float bigw = 0.f, bigm = 0.f;
     {
       float qk[4][4], kk2[4][4];
@@ -664,7 +664,7 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
           const float m0 = cc < r ? -da[i][e] * dec : 0.f;  // dA D
           const float mk = m0 * (ks * ks * kk2[i][e]);
           const float b = e >> 1 ? b1 : b0;
-          const float x = w * (qs * ks * qk[i][e]) + b * mk;
+          const float x = cc < r ? w * (qs * ks * qk[i][e]) + b * mk : 0.f;
           nb[e >> 1] += mk;
           rows[e >> 1] += x;
           cs[e & 1] += x;
@@ -752,9 +752,10 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
         // M's contribution to dbeta has beta left out, so that it holds for beta = 0 too.
         const float b = sm.xv[r] - sm.G[r] * (sm.zk[0][r] + sm.zk[1][r]) + sm.db[0][r] + sm.db[1][r];
         if (r < len) dbeta[(size_t)(t0 + r) * HV + h] = b;
-        d[i] = (double)sm.rows[0][r] + sm.rows[1][r] -
+        const double et = (double)sm.tail[0][r] + sm.tail[1][r];
+        d[i] = (double)sm.rows[0][r] + sm.rows[1][r] - et -
                ((double)sm.cols[0][r] + sm.cols[1][r] + sm.cols[2][r] + sm.cols[3][r]);
-        e += (double)sm.tail[0][r] + sm.tail[1][r];
+        e += et;
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);

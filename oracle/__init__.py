@@ -11,6 +11,8 @@ chunkwise evaluator is pinned against the recurrence.
 from .kda_oracle import (  # noqa: F401
     L2_EPS,
     gate,
+    gdr_recurrent,
+    gdr_recurrent_backward,
     kda_chunkwise,
     kda_chunkwise_backward,
     kda_decode_step,
@@ -18,7 +20,9 @@ from .kda_oracle import (  # noqa: F401
     kda_recurrent_backward,
     l2_normalize,
     output_epilogue,
+    output_epilogue_backward,
     prologue,
+    prologue_backward,
     short_conv,
     silu,
     state_from_abi,

@@ -464,3 +464,81 @@ def state_to_abi(S):
 def state_from_abi(S):
     """The ABI's ``[..., Dv, Dk]`` -> key-first ``[..., Dk, Dv]``."""
     return np.swapaxes(_f64(S), -1, -2)
+
+
+# ---------------------------------------------------------------------------
+# Gated delta rule with one decay per head, and the training path's adjoints
+# ---------------------------------------------------------------------------
+
+def _per_value_head(x, HV):
+    """[T, HK, D] -> [T, HV, D]: value head h uses key head h // (HV // HK)."""
+    x = _f64(x)
+    return np.repeat(x, HV // x.shape[1], axis=1)
+
+
+def gdr_recurrent(q, k, v, g, beta, scale=1.0, initial_state=None, cu_seqlens=None):
+    """:func:`kda_recurrent` with one log-decay per (token, value head), ``g``
+    [T, HV], and ``q``, ``k`` [T, HK, D] shared by groups of value heads."""
+    v = _f64(v)
+    T, HV, _ = v.shape
+    q, k = _per_value_head(q, HV), _per_value_head(k, HV)
+    g = np.broadcast_to(_f64(g)[..., None], q.shape)
+    return kda_recurrent(q, k, v, g, beta, scale, initial_state, cu_seqlens)
+
+
+def gdr_recurrent_backward(q, k, v, g, beta, do, d_final_state=None, scale=1.0,
+                           initial_state=None, cu_seqlens=None):
+    """Gradients of :func:`gdr_recurrent`: :func:`kda_recurrent_backward` with
+    the shared heads' gradients and the channels' decay gradients summed."""
+    v = _f64(v)
+    T, HV, _ = v.shape
+    HK = q.shape[1]
+    qr, kr = _per_value_head(q, HV), _per_value_head(k, HV)
+    gr = np.broadcast_to(_f64(g)[..., None], qr.shape)
+    dq, dk, dv, dg, dbeta, ds0 = kda_recurrent_backward(qr, kr, v, gr, beta, do, d_final_state,
+                                                        scale, initial_state, cu_seqlens)
+    dq, dk = (x.reshape(T, HK, HV // HK, -1).sum(2) for x in (dq, dk))
+    return dq, dk, dv, dg.sum(-1), dbeta, ds0
+
+
+def prologue_backward(x, w, dq, dk, dv, H, D, cu_seqlens=None, cache_in=None):
+    """Gradients of L = sum(dq * q) + sum(dk * k) + sum(dv * v) for the outputs
+    of :func:`prologue` (the new cache taken as a constant): ``(dx [T, C],
+    dw [C, 4], dcache [N, 3, C])``.  The chain rule step by step: L2 norm, SiLU,
+    conv."""
+    x, w = _f64(x), _f64(w)
+    T, C = x.shape
+    segs = _segments(T, cu_seqlens)
+    c, _ = short_conv(x, w, cu_seqlens, cache_in)
+    sig = 1.0 / (1.0 + np.exp(-c))
+    y = (c * sig).reshape(T, 3, H, D)
+    up = np.stack([_f64(dq), _f64(dk), _f64(dv)], axis=1)
+    norm = np.sqrt(np.sum(y * y, axis=-1, keepdims=True) + L2_EPS)
+    dy = up / norm - y * np.sum(up * y, axis=-1, keepdims=True) / norm ** 3
+    dy[:, 2] = up[:, 2]
+    dc = dy.reshape(T, C) * (sig + c * sig * (1.0 - sig))
+    dx, dw = np.zeros((T, C)), np.zeros((C, 4))
+    dcache = np.zeros((len(segs), 3, C))
+    for n, (a, b) in enumerate(segs):
+        past = np.zeros((3, C)) if cache_in is None else _f64(cache_in)[n]
+        row = np.concatenate([past, x[a:b]])
+        drow = np.zeros_like(row)
+        for j in range(4):
+            drow[j:j + b - a] += dc[a:b] * w[:, j]
+            dw[:, j] += np.sum(dc[a:b] * row[j:j + b - a], axis=0)
+        dcache[n], dx[a:b] = drow[:3], drow[3:]
+    return dx, dw, dcache
+
+
+def output_epilogue_backward(o, gate_preact, weight, d_out, eps=1e-5):
+    """Gradients of L = sum(d_out * out) for :func:`output_epilogue`:
+    ``(d_o, d_gate, d_weight)``."""
+    o, z, w, d = _f64(o), _f64(gate_preact), _f64(weight), _f64(d_out)
+    D = o.shape[-1]
+    rms = np.sqrt(np.mean(o * o, axis=-1, keepdims=True) + float(eps))
+    e = np.exp(-np.abs(z))
+    sig = np.where(z >= 0, 1.0 / (1.0 + e), e / (1.0 + e))
+    up = d * sig * w
+    d_o = up / rms - o * np.sum(up * o, axis=-1, keepdims=True) / (D * rms ** 3)
+    d_gate = d * w * o / rms * e / (1.0 + e) ** 2
+    return d_o, d_gate, np.sum((d * sig * o / rms).reshape(-1, D), axis=0)
