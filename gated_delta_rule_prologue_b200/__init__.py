@@ -648,51 +648,74 @@ def kda_output_epilogue(o, gate, weight, out, *, eps: float = 1e-5, stream=None)
 
 
 # ---- gated delta rule with one decay per head; backward of prologue and epilogue ----------
-# These functions check shapes as well: the kernels trust the sizes they are given.
+# These functions check shapes as well: the kernels trust the sizes they are given.  A decode
+# step's kernel takes a few microseconds, so the checks are written to cost little when they
+# pass: one expression per tensor, pointers handed over as plain integers.
 
-def _expect(device, *tensors):
-    """Each of (tensor, name, shape, dtype) is a contiguous tensor of that shape and dtype on
-    ``device``, the current CUDA device; a tensor that is None is left out."""
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be CUDA tensors, got {device}")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    for t, name, shape, dtype in tensors:
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _refuse(t, name, shape, dtype, device):
+    """The error for a tensor that is not a contiguous one of this shape and dtype on CUDA
+    device number ``device``."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the current device cuda:{device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _p(t, name, shape, dtype, device):
+    """Address of a contiguous tensor of this shape and dtype on the current device (None: 0)."""
+    if t is None:
+        return None
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != device
+            or not t.is_contiguous()):
+        _refuse(t, name, shape, dtype, device)
+    return t.data_ptr()
+
+
+def _cuda_device(t):
+    """Number of the current device, which the call's tensors must be on."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return torch.cuda.current_device()
+
+
+def _stream_of(stream, device):
+    return _raw_stream(device) if stream is None else stream.cuda_stream
+
+
+def _scratch(workspace, nbytes, device, like):
+    """Address and bytes of a workspace ("auto": ``nbytes`` from torch's caching allocator); the
+    third value keeps it alive until the call has been made."""
+    if workspace is None:
+        return None, 0, None
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    n = workspace.numel()
+    return _p(workspace, "workspace", (n,), torch.uint8, device), n, workspace
 
 
 def _gdr_sizes(q, v, cu_seqlens):
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v have three dimensions: tokens, heads, channels")
     T, HK, D = q.shape
-    return 1 if cu_seqlens is None else cu_seqlens.numel() - 1, T, HK, v.shape[1], D
+    return 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1, T, HK, v.shape[1], D
 
 
-def _gdr_expect(q, k, v, g, beta, cu_seqlens, N, T, HK, HV, D, *more):
-    f32 = torch.float32
-    _expect(q.device, (q, "q", (T, HK, D), q.dtype), (k, "k", (T, HK, D), q.dtype),
-            (v, "v", (T, HV, D), q.dtype), (g, "g", (T, HV), f32), (beta, "beta", (T, HV), f32),
-            (cu_seqlens, "cu_seqlens", (N + 1,), torch.int32), *more)
-
-
-def _workspace(workspace, nbytes, device):
-    if isinstance(workspace, str):
-        if workspace != "auto":
-            raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    if workspace is not None:
-        _expect(device, (workspace, "workspace", workspace.shape, torch.uint8))
-    return workspace, 0 if workspace is None else workspace.numel()
+def _gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev):
+    dt, qk, heads = q.dtype, (T, HK, D), (T, HV)
+    return (_p(q, "q", qk, dt, dev), _p(k, "k", qk, dt, dev), _p(v, "v", (T, HV, D), dt, dev),
+            _p(g, "g", heads, torch.float32, dev), _p(beta, "beta", heads, torch.float32, dev))
 
 
 def kda_gdr_recurrent(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=None,
@@ -700,24 +723,24 @@ def kda_gdr_recurrent(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=
     """Gated delta rule with one decay per head, token by token: writes ``o`` [T, HV, D] and
     optionally ``final_state`` (which may be ``initial_state``)."""
     N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
-    f32, sq = torch.float32, (N, HV, D, D)
-    _gdr_expect(q, k, v, g, beta, cu_seqlens, N, T, HK, HV, D, (o, "o", (T, HV, D), f32),
-                (initial_state, "initial_state", sq, f32), (final_state, "final_state", sq, f32))
-    _check(lib.kda_gdr_recurrent(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
-                                 _ptr(initial_state), _ptr(cu_seqlens), N, T, HK, HV, D, _dtype(q),
-                                 _ptr(o), _ptr(final_state), _stream(stream)))
+    dev, f32, sq = _cuda_device(q), torch.float32, (N, HV, D, D)
+    _check(lib.kda_gdr_recurrent(
+        *_gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev), scale,
+        _p(initial_state, "initial_state", sq, f32, dev),
+        _p(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, HK, HV, D, _dtype(q),
+        _p(o, "o", (T, HV, D), f32, dev), _p(final_state, "final_state", sq, f32, dev),
+        _stream_of(stream, dev)))
 
 
 def kda_gdr_decode_step(q, k, v, g, beta, state, o, *, scale: float = 1.0, stream=None):
     """One new token for each of N sequences (``q, k`` [N, HK, D], ``v, o`` [N, HV, D]);
     updates ``state`` [N, HV, D, D] in place."""
-    N, _, HK, HV, D = _gdr_sizes(q, v, None)
-    N = q.shape[0]
-    f32 = torch.float32
-    _gdr_expect(q, k, v, g, beta, None, N, N, HK, HV, D, (o, "o", (N, HV, D), f32),
-                (state, "state", (N, HV, D, D), f32))
-    _check(lib.kda_gdr_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
-                                   _ptr(state), N, HK, HV, D, _dtype(q), _ptr(o), _stream(stream)))
+    _, N, HK, HV, D = _gdr_sizes(q, v, None)
+    dev, f32 = _cuda_device(q), torch.float32
+    _check(lib.kda_gdr_decode_step(
+        *_gdr_inputs(q, k, v, g, beta, N, HK, HV, D, dev), scale,
+        _p(state, "state", (N, HV, D, D), f32, dev), N, HK, HV, D, _dtype(q),
+        _p(o, "o", (N, HV, D), f32, dev), _stream_of(stream, dev)))
 
 
 def kda_gdr_chunk_fwd_workspace_bytes(N: int, T: int, HK: int, HV: int, D: int,
@@ -735,18 +758,17 @@ def kda_gdr_chunk_fwd(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=
     tensor of :func:`kda_gdr_chunk_fwd_workspace_bytes` is used as given; ``None`` runs
     :func:`kda_gdr_recurrent`.  fp32 inputs and D below 64 run the recurrent form."""
     N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
-    f32, sq = torch.float32, (N, HV, D, D)
-    _gdr_expect(q, k, v, g, beta, cu_seqlens, N, T, HK, HV, D, (o, "o", (T, HV, D), f32),
-                (initial_state, "initial_state", sq, f32), (final_state, "final_state", sq, f32))
-    dt = _dtype(q)
+    dev, f32, sq, dt = _cuda_device(q), torch.float32, (N, HV, D, D), _dtype(q)
     nbytes = 0
-    if isinstance(workspace, str):
-        nbytes = int(lib.kda_gdr_chunk_fwd_workspace_bytes(N, T, HK, HV, D, dt))
-    workspace, nbytes = _workspace(workspace, nbytes, q.device)
-    _check(lib.kda_gdr_chunk_fwd_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
-                                    _ptr(initial_state), _ptr(cu_seqlens), N, T, HK, HV, D, dt,
-                                    _ptr(o), _ptr(final_state), _ptr(workspace), nbytes,
-                                    _stream(stream)))
+    if workspace is not None and isinstance(workspace, str):
+        nbytes = lib.kda_gdr_chunk_fwd_workspace_bytes(N, T, HK, HV, D, dt)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, q)
+    _check(lib.kda_gdr_chunk_fwd_ws(
+        *_gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev), scale,
+        _p(initial_state, "initial_state", sq, f32, dev),
+        _p(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, HK, HV, D, dt,
+        _p(o, "o", (T, HV, D), f32, dev), _p(final_state, "final_state", sq, f32, dev), ws, nbytes,
+        _stream_of(stream, dev)))
 
 
 def kda_gdr_chunk_bwd_workspace_bytes(N: int, T: int, HK: int, HV: int, D: int,
@@ -763,7 +785,8 @@ def kda_gdr_chunk_bwd(q, k, v, g, beta, d_o, *, scale: float = 1.0, initial_stat
     final_state).  Returns ``(dq, dk, dv, dg, dbeta, d_initial_state)``: the first three of q's
     dtype, the others fp32, the last None unless wanted; outputs not given are allocated."""
     N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
-    f32, sq = torch.float32, (N, HV, D, D)
+    dev, f32, sq, dt = _cuda_device(q), torch.float32, (N, HV, D, D), _dtype(q)
+    heads, qk, vo, act = (T, HV), (T, HK, D), (T, HV, D), q.dtype
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -771,22 +794,18 @@ def kda_gdr_chunk_bwd(q, k, v, g, beta, d_o, *, scale: float = 1.0, initial_stat
     dbeta = torch.empty_like(beta) if dbeta is None else dbeta
     if d_initial_state is None and want_d_initial_state:
         d_initial_state = torch.empty(sq, dtype=f32, device=q.device)
-    _gdr_expect(q, k, v, g, beta, cu_seqlens, N, T, HK, HV, D, (d_o, "d_o", (T, HV, D), f32),
-                (initial_state, "initial_state", sq, f32),
-                (d_final_state, "d_final_state", sq, f32), (dq, "dq", (T, HK, D), q.dtype),
-                (dk, "dk", (T, HK, D), q.dtype), (dv, "dv", (T, HV, D), q.dtype),
-                (dg, "dg", (T, HV), f32), (dbeta, "dbeta", (T, HV), f32),
-                (d_initial_state, "d_initial_state", sq, f32))
-    dt = _dtype(q)
     nbytes = 0
-    if isinstance(workspace, str):
-        nbytes = max(int(lib.kda_gdr_chunk_bwd_workspace_bytes(N, T, HK, HV, D, dt)), 16)
-    workspace, nbytes = _workspace(workspace, nbytes, q.device)
-    _check(lib.kda_gdr_chunk_bwd_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
-                                    _ptr(initial_state), _ptr(cu_seqlens), N, T, HK, HV, D, dt,
-                                    _ptr(d_o), _ptr(d_final_state), _ptr(dq), _ptr(dk), _ptr(dv),
-                                    _ptr(dg), _ptr(dbeta), _ptr(d_initial_state), _ptr(workspace),
-                                    nbytes, _stream(stream)))
+    if workspace is not None and isinstance(workspace, str):
+        nbytes = max(lib.kda_gdr_chunk_bwd_workspace_bytes(N, T, HK, HV, D, dt), 16)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, q)
+    _check(lib.kda_gdr_chunk_bwd_ws(
+        *_gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev), scale,
+        _p(initial_state, "initial_state", sq, f32, dev),
+        _p(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, HK, HV, D, dt,
+        _p(d_o, "d_o", vo, f32, dev), _p(d_final_state, "d_final_state", sq, f32, dev),
+        _p(dq, "dq", qk, act, dev), _p(dk, "dk", qk, act, dev), _p(dv, "dv", vo, act, dev),
+        _p(dg, "dg", heads, f32, dev), _p(dbeta, "dbeta", heads, f32, dev),
+        _p(d_initial_state, "d_initial_state", sq, f32, dev), ws, nbytes, _stream_of(stream, dev)))
     return dq, dk, dv, dg, dbeta, d_initial_state
 
 
@@ -801,23 +820,20 @@ def kda_prologue_bwd(x, conv_w, dq, dk, dv, dx, d_conv_w=None, *, H: int, D: int
     writes ``dx`` (x's dtype) and, where given, ``d_conv_w`` [3*H*D, 4] (fp32) and
     ``d_cache_in`` (x's dtype).  ``dq, dk, dv`` [T, H, D] share a dtype of their own."""
     T, C = x.shape[0], 3 * H * D
-    N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
-    f32 = torch.float32
-    _expect(x.device, (x, "x", (T, C), x.dtype), (conv_w, "conv_w", (C, 4), f32),
-            (dq, "dq", (T, H, D), dq.dtype), (dk, "dk", (T, H, D), dq.dtype),
-            (dv, "dv", (T, H, D), dq.dtype), (dx, "dx", (T, C), x.dtype),
-            (d_conv_w, "d_conv_w", (C, 4), f32), (cache_in, "cache_in", (N, 3, C), x.dtype),
-            (d_cache_in, "d_cache_in", (N, 3, C), x.dtype),
-            (cu_seqlens, "cu_seqlens", (N + 1,), torch.int32))
+    N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    dev, f32, act, gt, thd = _cuda_device(x), torch.float32, x.dtype, dq.dtype, (T, H, D)
     dt = _dtype(x)
     nbytes = 0
-    if isinstance(workspace, str) and d_conv_w is not None:
-        nbytes = int(lib.kda_prologue_bwd_workspace_bytes(N, T, H, D, dt))
-    workspace, nbytes = _workspace(workspace, nbytes, x.device)
-    _check(lib.kda_prologue_bwd(_ptr(x), _ptr(conv_w), _ptr(cache_in), _ptr(cu_seqlens), N, T, H, D,
-                                dt, _dtype(dq), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dx),
-                                _ptr(d_conv_w), _ptr(d_cache_in), _ptr(workspace), nbytes,
-                                _stream(stream)))
+    if d_conv_w is not None and isinstance(workspace, str):
+        nbytes = lib.kda_prologue_bwd_workspace_bytes(N, T, H, D, dt)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, x)
+    _check(lib.kda_prologue_bwd(
+        _p(x, "x", (T, C), act, dev), _p(conv_w, "conv_w", (C, 4), f32, dev),
+        _p(cache_in, "cache_in", (N, 3, C), act, dev),
+        _p(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, H, D, dt, _dtype(dq),
+        _p(dq, "dq", thd, gt, dev), _p(dk, "dk", thd, gt, dev), _p(dv, "dv", thd, gt, dev),
+        _p(dx, "dx", (T, C), act, dev), _p(d_conv_w, "d_conv_w", (C, 4), f32, dev),
+        _p(d_cache_in, "d_cache_in", (N, 3, C), act, dev), ws, nbytes, _stream_of(stream, dev)))
 
 
 def kda_output_epilogue_bwd_workspace_bytes(T: int, H: int, D: int) -> int:
@@ -831,16 +847,14 @@ def kda_output_epilogue_bwd(o, gate, weight, d_out, d_o, d_gate, d_weight=None, 
     ``d_gate`` (gate's dtype) and, where given, ``d_weight`` [D] (fp32)."""
     if o.dim() != 3:
         raise ValueError("o has three dimensions: tokens, heads, channels")
-    T, H, D = o.shape
-    f32, dt = torch.float32, gate.dtype
-    _expect(o.device, (o, "o", (T, H, D), f32), (gate, "gate", (T, H, D), dt),
-            (weight, "weight", (D,), f32), (d_out, "d_out", (T, H, D), dt),
-            (d_o, "d_o", (T, H, D), f32), (d_gate, "d_gate", (T, H, D), dt),
-            (d_weight, "d_weight", (D,), f32))
+    thd = T, H, D = o.shape
+    dev, f32, dt = _cuda_device(o), torch.float32, gate.dtype
     nbytes = 0
-    if isinstance(workspace, str) and d_weight is not None:
-        nbytes = int(lib.kda_output_epilogue_bwd_workspace_bytes(T, H, D))
-    workspace, nbytes = _workspace(workspace, nbytes, o.device)
-    _check(lib.kda_output_epilogue_bwd(_ptr(o), _ptr(gate), _ptr(weight), float(eps), _ptr(d_out), T,
-                                       H, D, _dtype(gate), _ptr(d_o), _ptr(d_gate), _ptr(d_weight),
-                                       _ptr(workspace), nbytes, _stream(stream)))
+    if d_weight is not None and isinstance(workspace, str):
+        nbytes = lib.kda_output_epilogue_bwd_workspace_bytes(T, H, D)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, o)
+    _check(lib.kda_output_epilogue_bwd(
+        _p(o, "o", thd, f32, dev), _p(gate, "gate", thd, dt, dev),
+        _p(weight, "weight", (D,), f32, dev), eps, _p(d_out, "d_out", thd, dt, dev), T, H, D,
+        _dtype(gate), _p(d_o, "d_o", thd, f32, dev), _p(d_gate, "d_gate", thd, dt, dev),
+        _p(d_weight, "d_weight", (D,), f32, dev), ws, nbytes, _stream_of(stream, dev)))

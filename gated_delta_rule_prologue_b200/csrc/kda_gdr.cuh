@@ -74,6 +74,34 @@ __host__ __device__ inline Layout layout(int N, int T, int HK, int HV, int D, bo
 // The log-decay as the chunked form takes it (NaN stays NaN).
 __device__ __forceinline__ float floor_g(float g) { return g < -256.f ? -256.f : g; }
 
+// gamma of a chunk's tokens in base-2 units (gamma / ln 2), as two floats each (their sum in fp64,
+// split), by one warp whose lane holds g of tokens 2 lane and 2 lane + 1 (0 behind the end).
+__device__ __forceinline__ void gamma_of(float ga, float gb, float2 *gamma) {
+  const int lane = threadIdx.x & 31;
+  const double b = gb;
+  double s = ga + b;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const double o = __shfl_up_sync(0xffffffffu, s, off);
+    if (lane >= off) s += o;
+  }
+  constexpr double kLog2e = 1.4426950408889634074;
+  const double a = (s - b) * kLog2e;
+  s *= kLog2e;
+  const float ah = (float)a, sh = (float)s;
+  *reinterpret_cast<float4 *>(gamma + 2 * lane) =
+      make_float4(ah, (float)(a - ah), sh, (float)(s - sh));
+}
+// exp(gamma_r - gamma_i): the difference of the two sums is off by 2^-24 of itself, the
+// approximate base-2 exponential by a few 2^-23.
+__device__ __forceinline__ float decay_between(float2 r, float2 i) {
+  return ex2_approx((r.x - i.x) + (r.y - i.y));
+}
+// g of a token of the chunk at g0 (its head's first value, `stride` apart).
+__device__ __forceinline__ float load_g(const float *g0, size_t stride, int t, int len) {
+  return t < len ? floor_g(__ldg(g0 + t * stride)) : 0.f;
+}
+
 // Sequence and chunk of a slot; false for a slot that no chunk has.
 __device__ __forceinline__ bool chunk_of_slot(const int32_t *cu, int N, int T, long long slot,
                                               int *status, int &n, int &bos, int &eos, int &c) {
@@ -123,23 +151,39 @@ __device__ __forceinline__ void cp_block(uint32_t dst, const uint8_t *src, uint3
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 // c += a b: a 16 x 16 (rows lane/4, +8), b 16 x 8, fp16 operands, fp32 sums.
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// c = a b, without the eight moves that clear c.
+__device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+// Four 8 x 8 blocks of accumulator layout, written transposed (a lane gives a row's address).
+__device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+// Barrier of the first `threads` threads that call it with this id (1 .. 15).
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // Two 8-column blocks (n0 .. n0 + 15) of a B operand for the 16 k-values from k0 on.

@@ -285,7 +285,7 @@ template <int D> struct LocalSmem {
                                                                            : 4 * kTriBytes;
   static constexpr uint32_t kSmall = kU + kUBytes;
   struct Small {
-    double gamma[C];
+    alignas(16) float2 gamma[C];
     float G[C], E[C], beta[C], us[C];  // us: scale of U's rows
     float rows[2][C];                  // per half: sums that dgamma and dbeta take per row
     float cols[4][C];                  // per row block: column sums
@@ -382,19 +382,9 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
       sm.E[tid] = vec[kVecE * C + tid];
       sm.beta[tid] = vec[kVecBeta * C + tid];
     }
-    if (warp == 7) {  // gamma as in the prep pass
-      const int ta = 2 * lane, tb = ta + 1;
-      const size_t at = (size_t)(t0 + ta) * HV + h;
-      const float ga = ta < len ? floor_g(__ldg(g + at)) : 0.f;
-      const float gb = tb < len ? floor_g(__ldg(g + at + HV)) : 0.f;
-      double s = (double)ga + gb;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += o;
-      }
-      sm.gamma[tb] = s;
-      sm.gamma[ta] = s - gb;
+    if (warp == 7) {
+      const float *g0 = g + (size_t)t0 * HV + h;
+      gamma_of(load_g(g0, HV, 2 * lane, len), load_g(g0, HV, 2 * lane + 1, len), sm.gamma);
     }
     // S and dS' as planes with one power of two per matrix; <dS', S> from the planes' values.
     Scale ss, ds;
@@ -651,7 +641,7 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
           mma(kk2[2 * np + 1], aa, b[2], b[3]);
         }
       }
-      const double gr[2] = {sm.gamma[r0], sm.gamma[r1]};
+      const float2 gr[2] = {sm.gamma[r0], sm.gamma[r1]};
       float nb[2] = {0.f, 0.f}, rows[2] = {0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -659,7 +649,7 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = e >> 1 ? r1 : r0, cc = 32 * half + 8 * i + col + (e & 1);
-          const float dec = cc <= r ? expf((float)(gr[e >> 1] - sm.gamma[cc])) : 0.f;
+          const float dec = cc <= r ? decay_between(gr[e >> 1], sm.gamma[cc]) : 0.f;
           const float w = cc <= r ? dp[i][e] * dec : 0.f;
           const float m0 = cc < r ? -da[i][e] * dec : 0.f;  // dA D
           const float mk = m0 * (ks * ks * kk2[i][e]);

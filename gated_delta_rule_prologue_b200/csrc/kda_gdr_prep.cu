@@ -1,14 +1,19 @@
 // Prep pass of the chunked gated delta rule (kda_gdr.cuh): everything of a chunk that no state
 // enters, for all chunks at once.  One CTA per (chunk, key head): the products K K^T and Q K^T
-// are shared by the key head's value heads and stay in registers; per value head the decay
-// matrix, P, A and T = (I + A)^-1 follow and go out as split fp16 tiles.
+// are shared by the key head's value heads and stay in registers (warps 0-3 and 4-7, 16 token rows
+// each); per value head warps 4-7 make P and warps 0-3 make A and T = (I + A)^-1, each writing
+// split fp16 tiles.
 //
-// T: the inverses of the four 16 x 16 diagonal blocks by forward substitution (one column per
-// thread), then [[X, 0], [-Y A21 X, Y]] from blocks X, Y of 16 to 32 and from 32 to 64, in fp32
-// on the CUDA cores.  The substitution's error is that of fp32; nothing is divided.
+// T by blocks of 16: the inverses D_i of the diagonal blocks by forward substitution in fp32 (one
+// column per lane, a block per warp), then, with warp j owning block column j,
+//     T_ij = -D_i (A_ij T_jj + ... + A_i,i-1 T_i-1,j),  i = j + 1 .. 3
+// on the tensor cores with split operands.  The products run transposed, T_ij^T = -(sum of
+// T_kj^T A_ik^T) D_i^T, because an accumulator then is the next product's A operand as it stands;
+// A and D are B operands read along their rows from shared memory.  Block substitution adds
+// nothing to the error of the element-wise one, and nothing is divided.
 //
-// Bound: the CTA's chain of barriers (products, substitution, four small products); several CTAs
-// per SM hide one another's.  Bytes: 2 x 64 x D in and out per key head, 33 KB out per value head.
+// Bound: latency.  A head takes three barriers of four warps; three CTAs per SM hide one another's.
+// Bytes: 2 x 64 x D in and out per key head, 33 KB out per value head.
 #include <type_traits>
 
 #include "kda_gdr.cuh"
@@ -18,24 +23,31 @@ namespace {
 using namespace gdr;
 
 constexpr int kThreads = 256;
-constexpr int kLd = C + 1;      // row stride of the fp32 matrices
-constexpr int kLdM = 33;
+constexpr int kLdD = 17;
 
 template <int D> struct PrepSmem {
-  union {
-    uint8_t tiles[2 * C * D * 2];        // K, Q (until the products are in registers)
-    struct {
-      float A[C][kLd], T[C][kLd], M[32][kLdM];
-    } m;
-  };
-  double gamma[C];
-  float beta[C];
+  uint8_t tiles[2 * C * D * 2];   // K, Q
+  uint8_t a[2 * kTriBytes];       // A hi, A lo (64 x 64 tiles); then T hi, T lo
+  uint8_t d[4][2][1024];          // D_i hi, lo: 16 rows x 32 bytes, pieces swapped in odd row quads
+  float diag[4][16][kLdD];        // A's diagonal blocks, then D_i, in fp32
+  alignas(16) float2 gamma[8][C];  // a copy per warp
+  float beta[4][C];
+  float before[8][C];             // per warp: decay from token i to the end of the block before its rows
+  float sa[C], sd[4];             // scales of A's rows and of the D_i
+  float tmax[4][C];               // per block column, the largest of T's rows
   float largest[2][8];
 };
 
-// Eight 16-bit values of a tile, scaled by a power of two and rounded to fp16 (exact for bf16
-// values of at least 2^-14 of the tile's largest, off by 2^-25 of it below).
-__device__ __forceinline__ uint4 to_f16(const uint4 &u, float inv, __nv_bfloat16) {
+// The largest magnitude of eight bf16 values, in both halves' running maxima.
+__device__ __forceinline__ __nv_bfloat162 max_abs(__nv_bfloat162 m, const uint4 &u) {
+  const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __hmax2(m, __habs2(h[i]));
+  return m;
+}
+// Eight bf16 values of a tile, scaled by a power of two and rounded to fp16 (exact for values of
+// at least 2^-14 of the tile's largest, off by 2^-25 of it below).
+__device__ __forceinline__ uint4 to_f16(const uint4 &u, float inv) {
   float2 f[4];
   widen_pairs(u, f, __nv_bfloat16{});
 #pragma unroll
@@ -44,7 +56,7 @@ __device__ __forceinline__ uint4 to_f16(const uint4 &u, float inv, __nv_bfloat16
 }
 
 template <typename Tin, int D>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 2)
 gdr_prep_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const float *__restrict__ g,
                 const float *__restrict__ beta, const int32_t *__restrict__ cu, int N, int T, int HK,
                 int HV, uint8_t *__restrict__ ws, Layout lay, int *status) {
@@ -58,40 +70,46 @@ gdr_prep_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const floa
   if (!in_range(status, slot, slots(N, T))) return;
   const int t0 = bos + c * C, len = min(C, eos - t0);
 
-  // The tiles as they are, zeros behind the sequence's end.
-  constexpr int kPieces = D / 8;  // 16-byte pieces per row
-  const uint32_t tiles = smem_addr(sm.tiles);
-  for (int i = tid; i < 2 * C * kPieces; i += kThreads) {
-    const int which = i / (C * kPieces), row = i / kPieces % C, c8 = i % kPieces;
-    const Tin *src = (which ? q : k) + ((size_t)(t0 + min(row, len - 1)) * HK + hk) * D + c8 * 8;
-    cp16(tiles + which * kq_tile_bytes(D) + tile_off(row, c8), src, row < len);
+  // The tiles, zeros behind the sequence's end: in registers until their scale is known (fp16
+  // inputs are used as they are).  The first head's g is on its way meanwhile.
+  constexpr int kPieces = D / 8;                       // 16-byte pieces per row
+  constexpr int kEach = C * kPieces / kThreads;        // pieces of each tile per thread
+  const int group = HV / HK;
+  const float *g0 = g + (size_t)t0 * HV + hk * group;
+  const float *beta0 = beta + (size_t)t0 * HV + hk * group;
+  uint4 x[2][kEach];
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = tid + i * kThreads, row = e / kPieces;
+      x[which][i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < len)
+        x[which][i] = __ldg(reinterpret_cast<const uint4 *>((which ? q : k) +
+                                                            ((size_t)(t0 + row) * HK + hk) * D) +
+                            e % kPieces);
+    }
+  float ga = load_g(g0, HV, 2 * lane, len), gb = load_g(g0, HV, 2 * lane + 1, len);
+  float ba = 0.f, bb = 0.f;  // beta of tokens lane, lane + 32
+  if (warp < 4) {
+    if (lane < len) ba = __ldg(beta0 + (size_t)lane * HV);
+    if (lane + 32 < len) bb = __ldg(beta0 + (size_t)(lane + 32) * HV);
   }
-  cp_commit();
-  cp_wait<0>();
-  __syncthreads();
-
-  // Scales: fp16 inputs are used as they are.
+  const uint32_t tiles = smem_addr(sm.tiles);
   float ks = 1.f, qs = 1.f;
-  uint8_t *kq = ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D);
   if constexpr (std::is_same<Tin, __nv_bfloat16>::value) {
-    float big[2] = {0.f, 0.f};
-#pragma unroll
-    for (int which = 0; which < 2; ++which)
-      for (int i = tid; i < C * kPieces; i += kThreads) {
-        float2 f[4];
-        widen_pairs(*reinterpret_cast<const uint4 *>(sm.tiles + which * kq_tile_bytes(D) + i * 16), f,
-                    __nv_bfloat16{});
-#pragma unroll
-        for (int e = 0; e < 4; ++e) big[which] = fmaxf(big[which], fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
-      }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
+      __nv_bfloat162 m = __float2bfloat162_rn(0.f);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1)
-        big[which] = fmaxf(big[which], __shfl_xor_sync(0xffffffffu, big[which], off));
-      if (lane == 0) sm.largest[which][warp] = big[which];
+      for (int i = 0; i < kEach; ++i) m = max_abs(m, x[which][i]);
+      float big = fmaxf(__low2float(m), __high2float(m));
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+      if (lane == 0) sm.largest[which][warp] = big;
     }
     __syncthreads();
+    float big[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       big[0] = fmaxf(big[0], sm.largest[0][i]);
@@ -101,19 +119,23 @@ gdr_prep_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const floa
     ks = sk.s;
     qs = sq.s;
 #pragma unroll
-    for (int which = 0; which < 2; ++which)
-      for (int i = tid; i < C * kPieces; i += kThreads) {
-        uint4 *p = reinterpret_cast<uint4 *>(sm.tiles + which * kq_tile_bytes(D) + i * 16);
-        const uint4 h = to_f16(*p, which ? sq.inv : sk.inv, __nv_bfloat16{});
-        *p = h;
-        *reinterpret_cast<uint4 *>(kq + which * kq_tile_bytes(D) + i * 16) = h;
-      }
-    __syncthreads();
-  } else {
-    for (int i = tid; i < 2 * C * kPieces; i += kThreads)
-      *reinterpret_cast<uint4 *>(kq + i * 16) = *reinterpret_cast<const uint4 *>(sm.tiles + i * 16);
+    for (int i = 0; i < kEach; ++i) {
+      x[0][i] = to_f16(x[0][i], sk.inv);
+      x[1][i] = to_f16(x[1][i], sq.inv);
+    }
   }
+  uint8_t *kq = ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D);
+#pragma unroll
+  for (int which = 0; which < 2; ++which)
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = tid + i * kThreads;
+      const uint32_t o = which * kq_tile_bytes(D) + tile_off(e / kPieces, e % kPieces);
+      *reinterpret_cast<uint4 *>(sm.tiles + o) = x[which][i];
+      *reinterpret_cast<uint4 *>(kq + o) = x[which][i];
+    }
   if (tid == 0) *reinterpret_cast<float2 *>(kq + 2 * kq_tile_bytes(D)) = make_float2(ks, qs);
+  __syncthreads();
 
   // Warps 0-3: rows 16 w of K K^T; warps 4-7: of Q K^T.  Blocks above the diagonal are not needed.
   const int w4 = warp & 3;
@@ -139,167 +161,263 @@ gdr_prep_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const floa
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[i][e] *= unit;
 
-  const int r0 = 16 * w4 + lane / 4, col = 2 * (lane & 3);
-  const int group = HV / HK;
+  const int r0 = 16 * w4 + lane / 4, r1 = r0 + 8, col = 2 * (lane & 3);
+  const uint32_t at_a = smem_addr(sm.a);
+  float2 *gamma = sm.gamma[warp];
+  const int last = 2 * w4 + 1;  // the warp's last 8-column block that reaches below the diagonal
   for (int j = 0; j < group; ++j) {
     const int h = hk * group + j;
-    __syncthreads();  // the tiles, or the previous head's matrices, have been read
-    if (warp == 0) {  // gamma: tokens 2 lane, 2 lane + 1
-      const int ta = 2 * lane, tb = ta + 1;
-      const size_t at = (size_t)(t0 + ta) * HV + h;
-      const float ga = ta < len ? floor_g(__ldg(g + at)) : 0.f;
-      const float gb = tb < len ? floor_g(__ldg(g + at + HV)) : 0.f;
-      double s = (double)ga + gb;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double o = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += o;
-      }
-      sm.gamma[tb] = s;
-      sm.gamma[ta] = s - gb;
-    } else if (warp == 1) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = lane + 32 * i;
-        sm.beta[t] = t < len ? __ldg(beta + (size_t)(t0 + t) * HV + h) : 0.f;
-      }
-    }
-    __syncthreads();
     uint8_t *tp = ws + lay.tp + (size_t)(slot * HV + h) * kTpBytes;
     float *vec = reinterpret_cast<float *>(tp + kVec);
-    const double gr[2] = {sm.gamma[r0], sm.gamma[r0 + 8]};
-    if (!is_q) {
-      const float br[2] = {sm.beta[r0], sm.beta[r0 + 8]};
+    __syncwarp();
+    gamma_of(ga, gb, gamma);
+    if (warp < 4) {
+      sm.beta[w4][lane] = ba;
+      sm.beta[w4][lane + 32] = bb;
+    }
+    __syncwarp();
+    if (j + 1 < group) {  // the next head's
+      ga = load_g(g0 + j + 1, HV, 2 * lane, len);
+      gb = load_g(g0 + j + 1, HV, 2 * lane + 1, len);
+      if (warp < 4) {
+        if (lane < len) ba = __ldg(beta0 + j + 1 + (size_t)lane * HV);
+        if (lane + 32 < len) bb = __ldg(beta0 + j + 1 + (size_t)(lane + 32) * HV);
+      }
+    }
+    // A row's decay since token i < 16 w4 is the decay from i to the end of the block before the
+    // warp's rows times that from there on: no factor is above 1, and one exponential per row and
+    // column does for all of them.
+    const float2 gr[2] = {gamma[r0], gamma[r1]};
+    float *before = sm.before[warp];
+    const float2 gs = gamma[max(16 * w4 - 1, 0)];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 2; ++i)
+      if (lane + 32 * i < 16 * w4) before[lane + 32 * i] = decay_between(gs, gamma[lane + 32 * i]);
+    __syncwarp();
+    float x[8][4];
+    zero(x);
+    const float b0 = is_q ? 1.f : sm.beta[w4][r0], b1 = is_q ? 1.f : sm.beta[w4][r1];
+    const float f0 = b0 * decay_between(gr[0], gs), f1 = b1 * decay_between(gr[1], gs);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = r0 + 8 * (e >> 1), cc = 8 * i + col + (e & 1);
-          sm.m.A[r][cc] = cc < r ? br[e >> 1] * expf((float)(gr[e >> 1] - sm.gamma[cc])) * acc[i][e] : 0.f;
-        }
-    } else {
-      float p[8][4];
+    for (int i = 0; i < 8; ++i) {
+      if (i > last) break;
+      if (i < 2 * w4) {
+        const float2 d = *reinterpret_cast<const float2 *>(before + 8 * i + col);
+        x[i][0] = f0 * acc[i][0] * d.x;
+        x[i][1] = f0 * acc[i][1] * d.y;
+        x[i][2] = f1 * acc[i][2] * d.x;
+        x[i][3] = f1 * acc[i][3] * d.y;
+        continue;
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int e = 0; e < 2; ++e) {
+        const int cc = 8 * i + col + e;
+        const float2 gc = gamma[cc];
+        const float d0 = decay_between(gr[0], gc), d1 = decay_between(gr[1], gc);
+        // P holds its diagonal, A does not.
+        if (cc < r0 + is_q) x[i][e] = b0 * d0 * acc[i][e];
+        if (cc < r1 + is_q) x[i][e + 2] = b1 * d1 * acc[i][e + 2];
+      }
+    }
+    Scale s0, s1;
+    row_scales(x, s0, s1);
+
+    if (is_q) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = r0 + 8 * (e >> 1), cc = 8 * i + col + (e & 1);
-          p[i][e] = cc <= r ? expf((float)(gr[e >> 1] - sm.gamma[cc])) * acc[i][e] : 0.f;
-        }
-      Scale s0, s1;
-      row_scales(p, s0, s1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 8; ++i) {
+        if (i > last) break;  // nothing above the 16 x 16 diagonal blocks is ever read
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           uint32_t hi, lo;
-          split2(p[i][2 * e], p[i][2 * e + 1], e ? s1.inv : s0.inv, hi, lo);
-          const uint32_t at = tile_off(r0 + 8 * e, i) + 2 * col;
-          *reinterpret_cast<uint32_t *>(tp + kP_HI + at) = hi;
-          *reinterpret_cast<uint32_t *>(tp + kP_LO + at) = lo;
+          split2(x[i][2 * e], x[i][2 * e + 1], e ? s1.inv : s0.inv, hi, lo);
+          const uint32_t o = tile_off(r0 + 8 * e, i) + 2 * col;
+          *reinterpret_cast<uint32_t *>(tp + kP_HI + o) = hi;
+          *reinterpret_cast<uint32_t *>(tp + kP_LO + o) = lo;
         }
+      }
       if ((lane & 3) == 0) {
         vec[kVecP * C + r0] = s0.s;
-        vec[kVecP * C + r0 + 8] = s1.s;
+        vec[kVecP * C + r1] = s1.s;
       }
+      const int t = 16 * w4 + (lane & 15);
+      if (lane < 16)
+        vec[kVecG * C + t] = ex2_approx(gamma[t].x + gamma[t].y);
+      else
+        vec[kVecE * C + t] = decay_between(gamma[C - 1], gamma[t]);
+      continue;
     }
-    if (tid < C) {
-      const double last = sm.gamma[C - 1];
-      vec[kVecG * C + tid] = expf((float)sm.gamma[tid]);
-      vec[kVecE * C + tid] = expf((float)(last - sm.gamma[tid]));
-      vec[kVecBeta * C + tid] = sm.beta[tid];
-    }
-    __syncthreads();
 
-    // T.  Diagonal blocks: thread = (block, column).
-    if (tid < C) {
-      const int b = tid & ~15, cc = tid & 15;
-      float x[16];
+    // A's rows of this warp as planes, its diagonal block in fp32 too.
+    if (lane < 16) vec[kVecBeta * C + 16 * w4 + lane] = sm.beta[w4][16 * w4 + lane];
+    if (j > 0) named_barrier(1, 128);  // the previous head's T has left the planes
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float t = r == cc ? 1.f : 0.f;
-#pragma unroll
-        for (int i = 0; i < r; ++i) t = fmaf(-sm.m.A[b + r][b + i], x[i], t);
-        x[r] = t;
-        sm.m.T[b + r][b + cc] = t;
-      }
-    }
-    __syncthreads();
-    // 16 -> 32: block rows 16..31 of each half, M = A21 X, then -Y M.
-    {
-      const int half = tid >> 7, r = (tid >> 3) & 15, c2 = 2 * (tid & 7), o = 32 * half;
-      float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float a = sm.m.A[o + 16 + r][o + i];
-        m0 = fmaf(a, sm.m.T[o + i][o + c2], m0);
-        m1 = fmaf(a, sm.m.T[o + i][o + c2 + 1], m1);
-      }
-      sm.m.M[16 * half + r][c2] = m0;
-      sm.m.M[16 * half + r][c2 + 1] = m1;
-      __syncthreads();
-      m0 = m1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float y = sm.m.T[o + 16 + r][o + 16 + i];
-        m0 = fmaf(y, sm.m.M[16 * half + i][c2], m0);
-        m1 = fmaf(y, sm.m.M[16 * half + i][c2 + 1], m1);
-      }
-      sm.m.T[o + 16 + r][o + c2] = -m0;
-      sm.m.T[o + 16 + r][o + c2 + 1] = -m1;
-      sm.m.T[o + r][o + 16 + c2] = 0.f;      // above the diagonal
-      sm.m.T[o + r][o + 16 + c2 + 1] = 0.f;
-    }
-    __syncthreads();
-    // 32 -> 64.
-    {
-      const int r = tid >> 3, c4 = 4 * (tid & 7);
-      float m[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
-        const float a = sm.m.A[32 + r][i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = fmaf(a, sm.m.T[i][c4 + e], m[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sm.m.M[r][c4 + e] = m[e];
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < 4; ++e) m[e] = 0.f;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
-        const float y = sm.m.T[32 + r][32 + i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) m[e] = fmaf(y, sm.m.M[i][c4 + e], m[e]);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sm.m.T[32 + r][c4 + e] = -m[e];
-    }
-    __syncthreads();
-    // Rows out: four threads per row, 16 columns each; nothing above the 16 x 16 diagonal blocks
-    // is ever read.
-    {
-      const int r = tid >> 2, b = tid & 3;
-      float x[16], big = 0.f;
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[e] = b <= r / 16 ? sm.m.T[r][16 * b + e] : 0.f;
-        big = fmaxf(big, fabsf(x[e]));
-      }
-      const Scale s = scale_of(quad_max(big));
-      uint32_t hi[8], lo[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) split2(x[2 * e], x[2 * e + 1], s.inv, hi[e], lo[e]);
+    for (int i = 0; i < 8; ++i) {
+      if (i > last) break;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t at = tile_off(r, 2 * b + e);
-        *reinterpret_cast<uint4 *>(tp + kT_HI + at) =
-            make_uint4(hi[4 * e], hi[4 * e + 1], hi[4 * e + 2], hi[4 * e + 3]);
-        *reinterpret_cast<uint4 *>(tp + kT_LO + at) =
-            make_uint4(lo[4 * e], lo[4 * e + 1], lo[4 * e + 2], lo[4 * e + 3]);
+        uint32_t hi, lo;
+        split2(x[i][2 * e], x[i][2 * e + 1], e ? s1.inv : s0.inv, hi, lo);
+        const uint32_t o = tile_off(r0 + 8 * e, i) + 2 * col;
+        *reinterpret_cast<uint32_t *>(sm.a + o) = hi;
+        *reinterpret_cast<uint32_t *>(sm.a + kTriBytes + o) = lo;
+        if (i >= last - 1) {
+          float *d = &sm.diag[w4][lane / 4 + 8 * e][8 * (i - last + 1) + col];
+          d[0] = x[i][2 * e];
+          d[1] = x[i][2 * e + 1];
+        }
       }
-      if (b == 0) vec[kVecT * C + r] = s.s;
     }
+    if ((lane & 3) == 0) {
+      sm.sa[r0] = s0.s;
+      sm.sa[r1] = s1.s;
+    }
+    __syncwarp();
+    // D_i of this warp's block: lane = column (lanes 16-31 repeat 0-15).
+    {
+      const int cc = lane & 15;
+      float x[16], big = 0.f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float t = r == cc ? 1.f : 0.f, t2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < r; ++i) {  // two sums: half the chain
+          float &s = i & 1 ? t2 : t;
+          s = fmaf(-sm.diag[w4][r][i], x[i], s);
+        }
+        x[r] = t + t2;
+        big = fmaxf(big, fabsf(x[r]));
+      }
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+      const Scale sd = scale_of(big);
+      __syncwarp();
+      if (lane < 16) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          sm.diag[w4][r][cc] = x[r];
+          const float v = x[r] * sd.inv;
+          const __half hi = __float2half_rn(v), lo = __float2half_rn(v - __half2float(hi));
+          const int o = r * 32 + (((cc >> 3) ^ ((r >> 2) & 1)) << 4) + 2 * (cc & 7);
+          *reinterpret_cast<__half *>(&sm.d[w4][0][o]) = hi;
+          *reinterpret_cast<__half *>(&sm.d[w4][1][o]) = lo;
+        }
+      }
+      if (lane == 0) sm.sd[w4] = sd.s;
+    }
+    named_barrier(1, 128);
+    // Block column w4 of T, transposed: tt[i] has rows c = 16 w4 + lane/4 (+8), columns r = 16 i ..
+    // T_kj is split once and enters the sums of all i > k; only the sum that T_k+1,j waits for is
+    // on the path to the next step.
+    float tt[4][2][4], sum[4][2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      zero(tt[i]);
+      zero(sum[i]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k < w4) continue;
+      if (k == w4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            tt[k][e][f] = sm.diag[w4][8 * e + col + (f & 1)][lane / 4 + 8 * (f >> 1)];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 s = *reinterpret_cast<const float2 *>(sm.sa + 16 * k + 8 * e + col);
+          sum[k][e][0] *= s.x; sum[k][e][1] *= s.y; sum[k][e][2] *= s.x; sum[k][e][3] *= s.y;
+        }
+        Scale t0s, t1s;
+        row_scales(sum[k], t0s, t1s);
+        uint32_t hi[4], lo[4], b[4], bl[4];
+        const int m = lane >> 3, r = (m >> 1) * 8 + (lane & 7);
+        const uint32_t o = r * 32 + (((m & 1) ^ ((r >> 2) & 1)) << 4);
+        ldsm4(b, smem_addr(sm.d[k][0]) + o);
+        ldsm4(bl, smem_addr(sm.d[k][1]) + o);
+        split_a(sum[k], 0, t0s, t1s, hi, lo);
+        float y[2][4], y2[2][4];  // two chains of MMAs
+        mma0(y[0], hi, b[0], b[1]);
+        mma0(y[1], hi, b[2], b[3]);
+        mma0(y2[0], lo, b[0], b[1]);
+        mma0(y2[1], lo, b[2], b[3]);
+        mma(y2[0], hi, bl[0], bl[1]);
+        mma(y2[1], hi, bl[2], bl[3]);
+        const float f0 = -sm.sd[k] * t0s.s, f1 = -sm.sd[k] * t1s.s;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int f = 0; f < 4; ++f) tt[k][e][f] = (f >> 1 ? f1 : f0) * (y[e][f] + y2[e][f]);
+      }
+      if (k == 3) continue;
+      Scale t0s, t1s;
+      row_scales(tt[k], t0s, t1s);
+      uint32_t hi[4], lo[4];
+      split_a(tt[k], 0, t0s, t1s, hi, lo);
+#pragma unroll
+      for (int i = k + 1; i < 4; ++i) {
+        uint32_t b[4], bl[4];
+        load_b(b, at_a, 16 * i, 16 * k);
+        load_b(bl, at_a + kTriBytes, 16 * i, 16 * k);
+        float y[2][4], y2[2][4];
+        mma0(y[0], hi, b[0], b[1]);
+        mma0(y[1], hi, b[2], b[3]);
+        mma0(y2[0], lo, b[0], b[1]);
+        mma0(y2[1], lo, b[2], b[3]);
+        mma(y2[0], hi, bl[0], bl[1]);
+        mma(y2[1], hi, bl[2], bl[3]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int f = 0; f < 4; ++f)
+            sum[i][e][f] = fmaf(f >> 1 ? t1s.s : t0s.s, y[e][f] + y2[e][f], sum[i][e][f]);
+      }
+    }
+    // Scales of T's rows (its columns are spread over the warps).
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < w4) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          float v = fmaxf(fabsf(tt[i][e][f]), fabsf(tt[i][e][f + 2]));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+          if (lane < 4) sm.tmax[w4][16 * i + 8 * e + col + f] = v;
+        }
+    }
+    named_barrier(1, 128);  // also: A's planes have been read
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < w4) continue;
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float inv[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int r = 16 * i + 8 * e + col + f;
+          float v = sm.tmax[0][r];
+#pragma unroll
+          for (int jj = 1; jj < 4; ++jj)
+            if (jj <= i) v = fmaxf(v, sm.tmax[jj][r]);
+          const Scale s = scale_of(v);
+          inv[f] = s.inv;
+          if (i == w4 && lane < 4) vec[kVecT * C + r] = s.s;
+        }
+        split2(tt[i][e][0] * inv[0], tt[i][e][1] * inv[1], 1.f, hi[2 * e], lo[2 * e]);
+        split2(tt[i][e][2] * inv[0], tt[i][e][3] * inv[1], 1.f, hi[2 * e + 1], lo[2 * e + 1]);
+      }
+      const int m = lane >> 3;
+      const uint32_t o = tile_off(16 * i + (m >> 1) * 8 + (lane & 7), 2 * w4 + (m & 1));
+      stsm4t(at_a + o, hi[0], hi[1], hi[2], hi[3]);
+      stsm4t(at_a + kTriBytes + o, lo[0], lo[1], lo[2], lo[3]);
+    }
+    named_barrier(1, 128);
+    for (int i = tid; i < 2 * kTriBytes / 16; i += 128)
+      *reinterpret_cast<uint4 *>(tp + kT_HI + i * 16) = *reinterpret_cast<const uint4 *>(sm.a + i * 16);
   }
 }
 
