@@ -21,9 +21,9 @@
 // Workspace: records of the chunks.  Chunk c of sequence n, whose first token is bos, has slot
 // bos / 64 + n + c (strictly increasing from chunk to chunk, so no index pass is needed; T / 64 +
 // N + 1 slots).
-//   KQ record (slot, key head):   K tile, Q tile: 64 rows x D fp16, 64-column blocks of 64 rows x
-//                                 128 bytes with the 16-byte pieces XOR-swizzled by the row;
-//                                 {2^eK, 2^eQ} as two floats
+//   KQ record (slot, key head):   one tile of 128 rows (K's tokens, then Q's) x D fp16: 64-column
+//                                 blocks of 128 rows x 128 bytes with the 16-byte pieces
+//                                 XOR-swizzled by the row; {2^eK, 2^eQ} as two floats
 //   TP record (slot, value head): T hi, T lo, P hi, P lo: 64 x 64 fp16 tiles, same layout, rows
 //                                 scaled; then fp32 [64]: G, E, 2^eT, 2^eP, beta
 #pragma once
@@ -45,8 +45,10 @@ constexpr uint32_t kT_HI = 0, kT_LO = kTriBytes, kP_HI = 2 * kTriBytes, kP_LO = 
 constexpr uint32_t kVec = 4 * kTriBytes;
 enum { kVecG = 0, kVecE = 1, kVecT = 2, kVecP = 3, kVecBeta = 4, kVecs = 5 };
 constexpr uint32_t kTpBytes = kVec + kVecs * C * 4;
-__host__ __device__ constexpr uint32_t kq_tile_bytes(int D) { return (uint32_t)C * D * 2; }
-__host__ __device__ constexpr uint32_t kq_bytes(int D) { return 2 * kq_tile_bytes(D) + 128; }
+constexpr int kKq = 2 * C;               // rows of the K and Q tile
+constexpr uint32_t kQRows = C * 128;     // byte offset of Q's first row in each column block
+__host__ __device__ constexpr uint32_t kq_tile_bytes(int D) { return (uint32_t)kKq * D * 2; }
+__host__ __device__ constexpr uint32_t kq_bytes(int D) { return kq_tile_bytes(D) + 128; }
 
 __host__ __device__ inline long long slots(int N, int T) { return (long long)T / C + N + 1; }
 __host__ __device__ inline long long first_slot(int bos, int n) { return bos / C + n; }
@@ -54,7 +56,8 @@ __host__ __device__ inline long long first_slot(int bos, int n) { return bos / C
 // Byte offsets in the workspace.
 struct Layout {
   size_t kq, tp;                 // records
-  size_t state, dstate, u, x;    // backward: per chunk fp32 S and dS' [D][D] (value-major), U and X [64][D]
+  size_t state, dstate, u, x;    // backward: per chunk fp32 S and dS' (key-major: [key][value channel]),
+                                 // U and X [64][D]
   size_t bytes;
 };
 __host__ __device__ inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
@@ -188,19 +191,22 @@ __device__ __forceinline__ void named_barrier(int id, int threads) {
 
 // Two 8-column blocks (n0 .. n0 + 15) of a B operand for the 16 k-values from k0 on.
 // Rows of the tile are B's columns (n), 16-byte pieces its k: r = {b0, b1, b0', b1'}.
+template <int R = C>
 __device__ __forceinline__ void load_b(uint32_t (&r)[4], uint32_t tile, int n0, int k0) {
   const int lane = threadIdx.x & 31, m = lane >> 3;
-  ldsm4(r, tile + tile_off(n0 + (m >> 1) * 8 + (lane & 7), (k0 >> 3) + (m & 1)));
+  ldsm4(r, tile + tile_off<R>(n0 + (m >> 1) * 8 + (lane & 7), (k0 >> 3) + (m & 1)));
 }
 // Rows of the tile are B's k.
-template <int R = C> __device__ __forceinline__ void load_bt(uint32_t (&r)[4], uint32_t tile, int n0, int k0) {
+template <int R = C>
+__device__ __forceinline__ void load_bt(uint32_t (&r)[4], uint32_t tile, int n0, int k0) {
   const int lane = threadIdx.x & 31, m = lane >> 3;
   ldsm4t(r, tile + tile_off<R>(k0 + (m & 1) * 8 + (lane & 7), (n0 >> 3) + (m >> 1)));
 }
 // A operand (16 rows from m0, 16 k from k0): rows of the tile are A's rows.
+template <int R = C>
 __device__ __forceinline__ void load_a(uint32_t (&r)[4], uint32_t tile, int m0, int k0) {
   const int lane = threadIdx.x & 31, m = lane >> 3;
-  ldsm4(r, tile + tile_off(m0 + (m & 1) * 8 + (lane & 7), (k0 >> 3) + (m >> 1)));
+  ldsm4(r, tile + tile_off<R>(m0 + (m & 1) * 8 + (lane & 7), (k0 >> 3) + (m >> 1)));
 }
 // Rows of the tile are A's k (the transposed tile is the operand).
 __device__ __forceinline__ void load_at(uint32_t (&r)[4], uint32_t tile, int m0, int k0) {
@@ -234,7 +240,8 @@ __device__ __forceinline__ void split2(float x, float y, float inv, uint32_t &hi
   const float2 v = __fmul2_rn(make_float2(x, y), make_float2(inv, inv));
   const __half2 h = __floats2half2_rn(v.x, v.y);
   const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(v.x - f.x, v.y - f.y);
+  const float2 r = __fadd2_rn(v, make_float2(-f.x, -f.y));
+  const __half2 l = __floats2half2_rn(r.x, r.y);
   hi = *reinterpret_cast<const uint32_t *>(&h);
   lo = *reinterpret_cast<const uint32_t *>(&l);
 }
@@ -267,7 +274,10 @@ template <int NT> __device__ __forceinline__ void zero(float (&c)[NT][4]) {
 
 }  // namespace gdr
 
-// Host side (kda_gdr_*.cu), called by kda_api.cu.
+// Host side (kda_gdr_*.cu), called by kda_api.cu; the *_tc form is launch_gdr_state's for D = 128.
+cudaError_t launch_gdr_state_tc(const void *v, const float *s0, const int32_t *cu, float scale, int N,
+                                int T, int HK, int HV, kda_dtype dt, void *ws, bool bwd, float *o,
+                                float *sN, int *status, cudaStream_t s);
 cudaError_t launch_gdr_prep(const void *q, const void *k, const float *g, const float *beta,
                             const int32_t *cu, int N, int T, int HK, int HV, int D, kda_dtype dt,
                             void *ws, bool bwd, int *status, cudaStream_t s);

@@ -32,8 +32,8 @@ using namespace gdr;
 
 template <int D, int NW> struct ReverseSmem {
   static constexpr int kLd = 16 * NW + 4;  // row stride of the dO tile: no bank conflicts
-  static constexpr uint32_t kK = 0, kQ = kq_tile_bytes(D);
-  static constexpr uint32_t kScales = 2 * kq_tile_bytes(D);
+  static constexpr uint32_t kK = 0, kQ = kQRows;
+  static constexpr uint32_t kScales = kq_tile_bytes(D);
   static constexpr uint32_t kTp = kq_bytes(D);
   static constexpr uint32_t kDo = kTp + kTpBytes;  // [64][kLd] fp32
   static constexpr uint32_t kStage = kDo + C * kLd * 4;
@@ -101,12 +101,11 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
     const size_t rec = (size_t)(slot0 + c) * HV + h;
 
     {
-      float *p = reinterpret_cast<float *>(ws + lay.dstate) + (rec * D + row) * D + col;
+      float *p = reinterpret_cast<float *>(ws + lay.dstate) + rec * D * D + row;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
-        *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
-      }
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[(8 * i + col + (e & 1)) * D + 8 * (e >> 1)] = s[i][e];
     }
     // (K dS')^T.
     float du[8][4];
@@ -120,7 +119,7 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t b[4];
-        load_b(b, st + Sm::kK, 16 * np, 16 * kk);
+        load_b<kKq>(b, st + Sm::kK, 16 * np, 16 * kk);
         mma(du[2 * np], hi, b[0], b[1]);
         mma(du[2 * np + 1], hi, b[2], b[3]);
         mma(du[2 * np], lo, b[0], b[1]);
@@ -238,12 +237,12 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
         uint32_t b[4];
-        load_bt(b, st + Sm::kQ, 16 * j, 16 * kk);
+        load_bt<kKq>(b, st + Sm::kQ, 16 * j, 16 * kk);
         mma(aq[0], qh[kk], b[0], b[1]);
         mma(aq[1], qh[kk], b[2], b[3]);
         mma(aq[0], ql[kk], b[0], b[1]);
         mma(aq[1], ql[kk], b[2], b[3]);
-        load_bt(b, st + Sm::kK, 16 * j, 16 * kk);
+        load_bt<kKq>(b, st + Sm::kK, 16 * j, 16 * kk);
         mma(ak[0], kh[kk], b[0], b[1]);
         mma(ak[1], kh[kk], b[2], b[3]);
         mma(ak[0], kl[kk], b[0], b[1]);
@@ -276,13 +275,12 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
 constexpr int kLocalThreads = 256;
 
 template <int D> struct LocalSmem {
-  static constexpr uint32_t kK = 0, kQ = kq_tile_bytes(D);
-  static constexpr uint32_t kSHi = 2 * kq_tile_bytes(D), kSLo = kSHi + D * D * 2;
+  static constexpr uint32_t kK = 0, kQ = kQRows;
+  static constexpr uint32_t kSHi = kq_tile_bytes(D), kSLo = kSHi + D * D * 2;
   static constexpr uint32_t kDHi = kSLo + D * D * 2, kDLo = kDHi + D * D * 2;
   static constexpr uint32_t kU = kDLo + D * D * 2;          // U hi, lo; later W hi, lo, M hi, lo
-  static constexpr uint32_t kULo = kU + kq_tile_bytes(D);
-  static constexpr uint32_t kUBytes = 2 * kq_tile_bytes(D) > 4 * kTriBytes ? 2 * kq_tile_bytes(D)
-                                                                           : 4 * kTriBytes;
+  static constexpr uint32_t kULo = kU + C * D * 2;
+  static constexpr uint32_t kUBytes = C * D * 4 > 4 * kTriBytes ? C * D * 4 : 4 * kTriBytes;
   static constexpr uint32_t kSmall = kU + kUBytes;
   struct Small {
     alignas(16) float2 gamma[C];
@@ -324,9 +322,9 @@ __device__ __forceinline__ float col_sum(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// fp16 pair at (row, column col of 8-column block c8) of a 64-row tile.
+// fp16 pair at (row, column col of 8-column block c8) of the K and Q tile.
 __device__ __forceinline__ float2 tile_pair(const uint8_t *tile, int row, int c8, int col) {
-  const uint32_t u = *reinterpret_cast<const uint32_t *>(tile + tile_off(row, c8) + 2 * col);
+  const uint32_t u = *reinterpret_cast<const uint32_t *>(tile + tile_off<kKq>(row, c8) + 2 * col);
   return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
@@ -356,10 +354,10 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
 
   {
     const uint8_t *kq = ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D);
-    cp_block(sb, kq, 2 * kq_tile_bytes(D));
+    cp_block(sb, kq, kq_tile_bytes(D));
     cp_commit();
     if (tid == 0) {
-      const float2 f = *reinterpret_cast<const float2 *>(kq + 2 * kq_tile_bytes(D));
+      const float2 f = *reinterpret_cast<const float2 *>(kq + kq_tile_bytes(D));
       sm.kq[0] = f.x;
       sm.kq[1] = f.y;
     }
@@ -501,8 +499,8 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
 #pragma unroll
         for (int np = 0; np < NH / 2; ++np) {
           uint32_t b[4], bl[4];
-          load_bt<D>(b, sb + Sm::kSHi, half * (D / 2) + 16 * np, 16 * kk);
-          load_bt<D>(bl, sb + Sm::kSLo, half * (D / 2) + 16 * np, 16 * kk);
+          load_b<D>(b, sb + Sm::kSHi, half * (D / 2) + 16 * np, 16 * kk);
+          load_b<D>(bl, sb + Sm::kSLo, half * (D / 2) + 16 * np, 16 * kk);
           mma(z[2 * np], hi, b[0], b[1]);
           mma(z[2 * np + 1], hi, b[2], b[3]);
           mma(z[2 * np], lo, b[0], b[1]);
@@ -593,8 +591,8 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
 #pragma unroll
         for (int np = 0; np < NH / 2; ++np) {
           uint32_t b[4], bl[4];
-          load_bt<D>(b, sb + Sm::kDHi, half * (D / 2) + 16 * np, 16 * kk);
-          load_bt<D>(bl, sb + Sm::kDLo, half * (D / 2) + 16 * np, 16 * kk);
+          load_b<D>(b, sb + Sm::kDHi, half * (D / 2) + 16 * np, 16 * kk);
+          load_b<D>(bl, sb + Sm::kDLo, half * (D / 2) + 16 * np, 16 * kk);
           mma(z[2 * np], hi, b[0], b[1]);
           mma(z[2 * np + 1], hi, b[2], b[3]);
           mma(z[2 * np], lo, b[0], b[1]);
@@ -628,13 +626,13 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
 #pragma unroll
       for (int kk = 0; kk < KK; ++kk) {
         uint32_t a[4], aa[4];
-        load_a(a, sb + Sm::kQ, 16 * m, 16 * kk);
-        load_a(aa, sb + Sm::kK, 16 * m, 16 * kk);
+        load_a<kKq>(a, sb + Sm::kQ, 16 * m, 16 * kk);
+        load_a<kKq>(aa, sb + Sm::kK, 16 * m, 16 * kk);
 #pragma unroll
         for (int np = 0; np < 2; ++np) {
           if (2 * half + np > m) break;
           uint32_t b[4];
-          load_b(b, sb + Sm::kK, 32 * half + 16 * np, 16 * kk);
+          load_b<kKq>(b, sb + Sm::kK, 32 * half + 16 * np, 16 * kk);
           mma(qk[2 * np], a, b[0], b[1]);
           mma(qk[2 * np + 1], a, b[2], b[3]);
           mma(kk2[2 * np], aa, b[0], b[1]);
@@ -717,7 +715,7 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
 #pragma unroll
         for (int np = 0; np < NH / 2; ++np) {
           uint32_t b[4];
-          load_bt(b, tile, half * (D / 2) + 16 * np, 16 * kk);
+          load_bt<kKq>(b, tile, half * (D / 2) + 16 * np, 16 * kk);
           mma(z[2 * np], hi, b[0], b[1]);
           mma(z[2 * np + 1], hi, b[2], b[3]);
           mma(z[2 * np], lo, b[0], b[1]);

@@ -130,11 +130,11 @@ gdr_prep_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const floa
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int e = tid + i * kThreads;
-      const uint32_t o = which * kq_tile_bytes(D) + tile_off(e / kPieces, e % kPieces);
+      const uint32_t o = which * kQRows + tile_off<kKq>(e / kPieces, e % kPieces);
       *reinterpret_cast<uint4 *>(sm.tiles + o) = x[which][i];
       *reinterpret_cast<uint4 *>(kq + o) = x[which][i];
     }
-  if (tid == 0) *reinterpret_cast<float2 *>(kq + 2 * kq_tile_bytes(D)) = make_float2(ks, qs);
+  if (tid == 0) *reinterpret_cast<float2 *>(kq + kq_tile_bytes(D)) = make_float2(ks, qs);
   __syncthreads();
 
   // Warps 0-3: rows 16 w of K K^T; warps 4-7: of Q K^T.  Blocks above the diagonal are not needed.
@@ -145,12 +145,12 @@ gdr_prep_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const floa
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
     uint32_t a[4];
-    load_a(a, tiles + (is_q ? kq_tile_bytes(D) : 0), 16 * w4, 16 * kk);
+    load_a<kKq>(a, tiles + (is_q ? kQRows : 0), 16 * w4, 16 * kk);
 #pragma unroll
     for (int np = 0; np < 4; ++np) {
       if (np > w4) break;
       uint32_t b[4];
-      load_b(b, tiles, 16 * np, 16 * kk);
+      load_b<kKq>(b, tiles, 16 * np, 16 * kk);
       mma(acc[2 * np], a, b[0], b[1]);
       mma(acc[2 * np + 1], a, b[2], b[3]);
     }

@@ -18,6 +18,9 @@
 // quarter (527 TFLOP/s measured over the GPU); with eight warps (a whole head) per CTA that is
 // what bounds the pass when there are chains enough, and with fewer chains than SMs a chain's
 // latency does.  Then a head is split over two CTAs of four warps, one per SM quarter.
+#include <stdlib.h>
+#include <type_traits>
+
 #include "kda_gdr.cuh"
 
 namespace kda {
@@ -25,8 +28,8 @@ namespace {
 using namespace gdr;
 
 template <int D, int NW> struct StateSmem {
-  static constexpr uint32_t kK = 0, kQ = kq_tile_bytes(D);
-  static constexpr uint32_t kScales = 2 * kq_tile_bytes(D);
+  static constexpr uint32_t kK = 0, kQ = kQRows;
+  static constexpr uint32_t kScales = kq_tile_bytes(D);
   static constexpr uint32_t kTp = kq_bytes(D);
   static constexpr uint32_t kV = kTp + kTpBytes;               // [64][16 NW] 16-bit, swizzled
   static constexpr uint32_t kStage = kV + C * 32 * NW;
@@ -109,13 +112,11 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
     const int t0 = bos + c * C, len = min(C, eos - t0);
 
     if constexpr (kKeep) {
-      float *p = reinterpret_cast<float *>(ws + lay.state) +
-                 (((size_t)(slot0 + c) * HV + h) * D + row) * D + col;
+      float *p = reinterpret_cast<float *>(ws + lay.state) + ((size_t)(slot0 + c) * HV + h) * D * D + row;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
-        *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
-      }
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[(8 * i + col + (e & 1)) * D + 8 * (e >> 1)] = s[i][e];
     }
 
     // (K S)^T and (Q S)^T.
@@ -131,13 +132,13 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t b[4];
-        load_b(b, st + Sm::kK, 16 * np, 16 * kk);
+        load_b<kKq>(b, st + Sm::kK, 16 * np, 16 * kk);
         mma(ks[2 * np], hi, b[0], b[1]);
         mma(ks[2 * np + 1], hi, b[2], b[3]);
         mma(ks[2 * np], lo, b[0], b[1]);
         mma(ks[2 * np + 1], lo, b[2], b[3]);
         if constexpr (!kKeep) {
-          load_b(b, st + Sm::kQ, 16 * np, 16 * kk);
+          load_b<kKq>(b, st + Sm::kQ, 16 * np, 16 * kk);
           mma(qs[2 * np], hi, b[0], b[1]);
           mma(qs[2 * np + 1], hi, b[2], b[3]);
           mma(qs[2 * np], lo, b[0], b[1]);
@@ -263,7 +264,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
 #pragma unroll
         for (int np = 0; np < 2; ++np) {
           uint32_t b[4];
-          load_bt(b, st + Sm::kK, 32 * j + 16 * np, 16 * kk);
+          load_bt<kKq>(b, st + Sm::kK, 32 * j + 16 * np, 16 * kk);
           mma(acc[2 * np], hi[kk], b[0], b[1]);
           mma(acc[2 * np + 1], hi[kk], b[2], b[3]);
           mma(acc[2 * np], lo[kk], b[0], b[1]);
@@ -314,6 +315,8 @@ cudaError_t launch_d(int D, const void *v, const float *s0, const int32_t *cu, f
   if (D == 64)
     return launch_nw<Tin, 64, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
   if (D != 128) return cudaErrorInvalidValue;
+  static const bool old = getenv("GDR_OLD") != nullptr;
+  if (!old) return launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, sizeof(Tin) == 2 && std::is_same<Tin, __half>::value ? KDA_F16 : KDA_BF16, ws, kKeep, o, sN, status, s);
   // Two CTAs per head as long as they all run at once (one per SM).
   if ((long long)N * HV * 2 <= 148)
     return launch_nw<Tin, 128, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
