@@ -19,7 +19,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowsInFlight = 2;
-constexpr int kMaxCtas = 148 * 6;  // one wave at six CTAs per SM
+constexpr int kMaxCtas = 148 * 4;  // one wave (64 registers: four CTAs per SM)
 
 template <typename T> struct Quad { uint2 u; };
 template <> struct Quad<float> { float4 u; };
@@ -119,26 +119,29 @@ epilogue_bwd_kernel(const float *__restrict__ o, const Tg *__restrict__ gate,
   }
 }
 
-// d_weight[c] = sum of the CTAs' rows: 1024/D slices of the rows each summed in order, then
-// the slices in order (fp64: a few hundred values per channel).
+// d_weight[c] = sum of the CTAs' rows: eight channels per CTA, 32 slices of the rows each summed
+// in order, then the slices in order (fp64: a few hundred values per channel).
 template <int D>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(256)
 epilogue_bwd_weight_kernel(const float *__restrict__ partial, int n, float *__restrict__ d_weight) {
-  constexpr int kSlices = 1024 / D;
-  __shared__ double part[1024];
-  const int c = threadIdx.x % D, slice = threadIdx.x / D;
+  __shared__ double part[32][8];
+  const int c = threadIdx.x & 7, slice = threadIdx.x >> 3;
+  const float *p = partial + 8 * blockIdx.x + c;
   double t = 0.0;
-  for (int i = slice; i < n; i += kSlices) t += (double)partial[(size_t)i * D + c];
-  part[threadIdx.x] = t;
+#pragma unroll 4
+  for (int i = slice; i < n; i += 32) t += (double)__ldg(p + (size_t)i * D);
+  part[slice][c] = t;
   __syncthreads();
   if (slice == 0) {
-    for (int i = 1; i < kSlices; ++i) t += part[i * D + c];
-    d_weight[c] = (float)t;
+    for (int i = 1; i < 32; ++i) t += part[i][c];
+    d_weight[8 * blockIdx.x + c] = (float)t;
   }
 }
 
 int ctas_of(long long rows, int D) {
   const long long per_cta = (long long)kWarps * (128 / D) * kRowsInFlight;
+  // A few trips of one CTA take less than the second kernel's launch.
+  if (rows <= 4 * per_cta) return rows > 0 ? 1 : 0;
   const long long want = (rows + per_cta - 1) / per_cta;
   return (int)(want < kMaxCtas ? want : kMaxCtas);
 }
@@ -155,7 +158,7 @@ cudaError_t launch_typed(const float *o, const void *gate, const float *weight, 
         o, static_cast<const Tg *>(gate), weight, eps, static_cast<const Tg *>(d_out), rows, d_o,
         static_cast<Tg *>(d_gate), partial);
   if (d_weight != nullptr && ctas != 1)
-    epilogue_bwd_weight_kernel<D><<<1, 1024, 0, s>>>(ws, ctas, d_weight);
+    epilogue_bwd_weight_kernel<D><<<D / 8, 256, 0, s>>>(ws, ctas, d_weight);
   return cudaGetLastError();
 }
 

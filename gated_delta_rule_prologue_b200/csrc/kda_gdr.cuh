@@ -184,11 +184,6 @@ __device__ __forceinline__ void stsm4t(uint32_t addr, uint32_t r0, uint32_t r1, 
                "r"(r0), "r"(r1), "r"(r2), "r"(r3)
                : "memory");
 }
-// Barrier of the first `threads` threads that call it with this id (1 .. 15).
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // Two 8-column blocks (n0 .. n0 + 15) of a B operand for the 16 k-values from k0 on.
 // Rows of the tile are B's columns (n), 16-byte pieces its k: r = {b0, b1, b0', b1'}.
 template <int R = C>

@@ -11,8 +11,8 @@
 // tokens of one sequence at a time: three inputs and three dc behind it live in registers, so
 // x, dn and dx are touched once.  dx_{t-3} is complete when dc_t is known, so a tile walks three
 // tokens past its end (their dc is recomputed by the next tile; nothing is exchanged).  The two
-// sums of the norm are xor shuffles over the D/4 lanes of a head.  The next kBatch tokens' rows
-// are loaded before the current ones are used.
+// sums of the norm are xor shuffles over the D/4 lanes of a head, for two tokens at a time.  The
+// next kAhead tokens' rows are on their way while the current ones are used.
 //
 // dw: a thread sums its channels' four taps over the tile in fp32 and writes them to the
 // workspace, [tile][channel][tap]; a second kernel adds the tiles in a fixed order (fp64).  The
@@ -27,7 +27,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;
+constexpr int kAhead = 4;  // tokens whose rows are on their way (a multiple of two)
 
 template <typename T> struct Quad { uint2 u; };
 template <> struct Quad<float> { float4 u; };
@@ -62,6 +62,36 @@ template <typename T> __device__ __forceinline__ Quad<T> load_quad(const T *p) {
   return r;
 }
 
+// r and m of two tokens (dy = r g + m y) from the lanes' parts of sum y^2 and of <y, g>: the four
+// sums over a head's G lanes are folded into one another (each lane ends up with one sum of one
+// token), a lane finishes its token's r and m, and the tokens' values are exchanged: nine shuffles
+// for G = 32 where four separate reductions take twenty.
+template <int G>
+__device__ __forceinline__ void norm_pair(const float2 (&ss)[2], const float2 (&dot)[2], bool norm,
+                                          float (&r)[2], float (&m)[2]) {
+  const int lane = threadIdx.x & 31;
+  const bool second = lane & (G / 2), is_dot = lane & (G / 4);
+  const float s0 = ss[0].x + ss[0].y, s1 = ss[1].x + ss[1].y;
+  const float d0 = dot[0].x + dot[0].y, d1 = dot[1].x + dot[1].y;
+  const float s = (second ? s1 : s0) + __shfl_xor_sync(0xffffffffu, second ? s0 : s1, G / 2);
+  const float d = (second ? d1 : d0) + __shfl_xor_sync(0xffffffffu, second ? d0 : d1, G / 2);
+  float v = (is_dot ? d : s) + __shfl_xor_sync(0xffffffffu, is_dot ? s : d, G / 4);
+#pragma unroll
+  for (int off = G / 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  const float o = __shfl_xor_sync(0xffffffffu, v, G / 4);
+  float rr = rsqrtf((is_dot ? o : v) + 1e-6f);
+  float mm = -rr * rr * rr * (is_dot ? v : o);
+  if (!norm) {
+    rr = 1.f;
+    mm = 0.f;
+  }
+  const float ro = __shfl_xor_sync(0xffffffffu, rr, G / 2), mo = __shfl_xor_sync(0xffffffffu, mm, G / 2);
+  r[0] = second ? ro : rr;
+  r[1] = second ? rr : ro;
+  m[0] = second ? mo : mm;
+  m[1] = second ? mm : mo;
+}
+
 template <typename Tin, typename Tg, int D>
 __global__ void __launch_bounds__(kThreads, 2)
 prologue_bwd_kernel(const Tin *__restrict__ x, const float *__restrict__ w,
@@ -77,6 +107,7 @@ prologue_bwd_kernel(const Tin *__restrict__ x, const float *__restrict__ w,
   const Tg *dn_base = p == 0 ? dq : (p == 1 ? dk : dv);
   const int cg = active ? c0 % HD : 0;  // the channel within q, k or v
   const bool norm = p < 2;
+  const bool norm_warp = __any_sync(0xffffffffu, norm);  // a warp of v's channels has no sums to make
 
   // The history of a sequence without tokens reaches no output.
   if (blockIdx.y == 0 && d_cache != nullptr && active) {
@@ -135,78 +166,89 @@ prologue_bwd_kernel(const Tin *__restrict__ x, const float *__restrict__ w,
       unpack(r, xh[j]);
       ch[j][0] = ch[j][1] = make_float2(0.f, 0.f);
     }
-    Quad<Tin> xr[kBatch];
-    Quad<Tg> gr[kBatch];
+    Quad<Tin> xr[kAhead];
+    Quad<Tg> gr[kAhead];
     auto fetch = [&](int t, Quad<Tin> &a, Quad<Tg> &b) {
       const bool ok = active && t < last && in_range(status, t, T);
       a = ok ? load_quad(x + (size_t)t * Cn + c0) : zero_quad<Tin>();
       b = ok ? load_quad(dn_base + (size_t)t * HD + cg) : zero_quad<Tg>();
     };
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) fetch(ta + i, xr[i], gr[i]);
-    for (int tt = ta; tt < tb + 3; tt += kBatch) {
+    for (int i = 0; i < kAhead; ++i) fetch(ta + i, xr[i], gr[i]);
+    for (int tt = ta; tt < tb + 3; tt += kAhead) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int t = tt + i;
-        float2 xf[2], g[2], c[2], s[2], y[2], dc[2];
-        unpack(xr[i], xf);
-        unpack(gr[i], g);
-        fetch(t + kBatch, xr[i], gr[i]);
-        float2 ss2 = make_float2(0.f, 0.f), dot2 = ss2;
+      for (int i = 0; i < kAhead; i += 2) {
+        const int t = tt + i;  // tokens t and t + 1
+        float2 xf[2][2], g[2][2], s[2][2], y[2][2], ss[2], dot[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float2 a = __fmul2_rn(wt[0][e], xh[0][e]);
-          a = __ffma2_rn(wt[1][e], xh[1][e], a);
-          a = __ffma2_rn(wt[2][e], xh[2][e], a);
-          c[e] = __ffma2_rn(wt[3][e], xf[e], a);
-          s[e].x = rcp_approx(1.f + ex2_approx(-1.4426950408889634f * c[e].x));
-          s[e].y = rcp_approx(1.f + ex2_approx(-1.4426950408889634f * c[e].y));
-          y[e] = __fmul2_rn(c[e], s[e]);
-          ss2 = __ffma2_rn(y[e], y[e], ss2);
-          dot2 = __ffma2_rn(y[e], g[e], dot2);
+        for (int k = 0; k < 2; ++k) {
+          unpack(xr[i + k], xf[k]);
+          unpack(gr[i + k], g[k]);
+          fetch(t + k + kAhead, xr[i + k], gr[i + k]);
         }
-        float ss = ss2.x + ss2.y, dot = dot2.x + dot2.y;
 #pragma unroll
-        for (int off = G / 2; off > 0; off >>= 1) {
-          ss += __shfl_xor_sync(0xffffffffu, ss, off);
-          dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        }
-        const float r = norm ? rsqrtf(ss + 1e-6f) : 1.f;
-        const float m = norm ? -r * r * r * dot : 0.f;  // dy = r g + m y
-        const bool in_seq = t < last;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float2 dy = __fmul2_rn(make_float2(r, r), g[e]);
-          dy = __ffma2_rn(make_float2(m, m), y[e], dy);
-          // s (1 + c (1 - s)) = s + y (1 - s)
-          const float2 om = __fadd2_rn(make_float2(1.f, 1.f), make_float2(-s[e].x, -s[e].y));
-          dc[e] = __fmul2_rn(dy, __ffma2_rn(y[e], om, s[e]));
-          if (!in_seq) dc[e] = make_float2(0.f, 0.f);
-          if (t < tb) {
-            dw[0][e] = __ffma2_rn(dc[e], xh[0][e], dw[0][e]);
-            dw[1][e] = __ffma2_rn(dc[e], xh[1][e], dw[1][e]);
-            dw[2][e] = __ffma2_rn(dc[e], xh[2][e], dw[2][e]);
-            dw[3][e] = __ffma2_rn(dc[e], xf[e], dw[3][e]);
-          }
-        }
-        const int td = t - 3;  // dx_{t-3} is complete
-        if (active && td < tb && (td >= ta || (d_cache != nullptr && ta == bos))) {
-          float2 d[2];
+        for (int k = 0; k < 2; ++k) {
+          ss[k] = dot[k] = make_float2(0.f, 0.f);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            d[e] = __fmul2_rn(wt[3][e], ch[0][e]);
-            d[e] = __ffma2_rn(wt[2][e], ch[1][e], d[e]);
-            d[e] = __ffma2_rn(wt[1][e], ch[2][e], d[e]);
-            d[e] = __ffma2_rn(wt[0][e], dc[e], d[e]);
+            float2 a = __fmul2_rn(wt[0][e], xh[k][e]);
+            a = __ffma2_rn(wt[1][e], xh[k + 1][e], a);
+            a = __ffma2_rn(wt[2][e], k ? xf[0][e] : xh[2][e], a);
+            const float2 c = __ffma2_rn(wt[3][e], xf[k][e], a);
+            s[k][e] = __fmul2_rn(c, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+            s[k][e].x = ex2_approx(s[k][e].x);
+            s[k][e].y = ex2_approx(s[k][e].y);
+            s[k][e] = __fadd2_rn(s[k][e], make_float2(1.f, 1.f));
+            s[k][e].x = rcp_approx(s[k][e].x);
+            s[k][e].y = rcp_approx(s[k][e].y);
+            y[k][e] = __fmul2_rn(c, s[k][e]);
+            ss[k] = __ffma2_rn(y[k][e], y[k][e], ss[k]);
+            dot[k] = __ffma2_rn(y[k][e], g[k][e], dot[k]);
           }
-          Tin *to = td >= ta ? dx + (size_t)td * Cn + c0
-                             : d_cache + ((size_t)n * 3 + (td - bos + 3)) * Cn + c0;
-          *reinterpret_cast<Quad<Tin> *>(to) = pack<Tin>(d);
         }
+        float r[2] = {1.f, 1.f}, m[2] = {0.f, 0.f};  // dy = r g + m y
+        if (norm_warp) norm_pair<G>(ss, dot, norm, r, m);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          xh[0][e] = xh[1][e]; xh[1][e] = xh[2][e]; xh[2][e] = xf[e];
-          ch[0][e] = ch[1][e]; ch[1][e] = ch[2][e]; ch[2][e] = dc[e];
+        for (int k = 0; k < 2; ++k) {
+          const bool in_seq = t + k < last, own = t + k < tb;
+          float2 dc[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float2 dy = __fmul2_rn(make_float2(r[k], r[k]), g[k][e]);
+            dy = __ffma2_rn(make_float2(m[k], m[k]), y[k][e], dy);
+            // s (1 + c (1 - s)) = s + y (1 - s)
+            const float2 om = __fadd2_rn(make_float2(1.f, 1.f), make_float2(-s[k][e].x, -s[k][e].y));
+            dc[e] = __fmul2_rn(dy, __ffma2_rn(y[k][e], om, s[k][e]));
+            if (!in_seq) dc[e] = make_float2(0.f, 0.f);
+          }
+          if (own) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              dw[0][e] = __ffma2_rn(dc[e], xh[0][e], dw[0][e]);
+              dw[1][e] = __ffma2_rn(dc[e], xh[1][e], dw[1][e]);
+              dw[2][e] = __ffma2_rn(dc[e], xh[2][e], dw[2][e]);
+              dw[3][e] = __ffma2_rn(dc[e], xf[k][e], dw[3][e]);
+            }
+          }
+          const int td = t + k - 3;  // dx_{t-3} is complete
+          if (active && td < tb && (td >= ta || (d_cache != nullptr && ta == bos))) {
+            float2 d[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              d[e] = __fmul2_rn(wt[3][e], ch[0][e]);
+              d[e] = __ffma2_rn(wt[2][e], ch[1][e], d[e]);
+              d[e] = __ffma2_rn(wt[1][e], ch[2][e], d[e]);
+              d[e] = __ffma2_rn(wt[0][e], dc[e], d[e]);
+            }
+            Tin *to = td >= ta ? dx + (size_t)td * Cn + c0
+                               : d_cache + ((size_t)n * 3 + (td - bos + 3)) * Cn + c0;
+            *reinterpret_cast<Quad<Tin> *>(to) = pack<Tin>(d);
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            xh[0][e] = xh[1][e]; xh[1][e] = xh[2][e]; xh[2][e] = xf[k][e];
+            ch[0][e] = ch[1][e]; ch[1][e] = ch[2][e]; ch[2][e] = dc[e];
+          }
         }
       }
     }
@@ -248,12 +290,21 @@ prologue_bwd_weight_kernel(const float4 *__restrict__ partial, int tiles, int Cn
 
 int channel_blocks(int Cn) { return (Cn / 4 + kThreads - 1) / kThreads; }
 
-// Tokens per tile: as long as the grid still gives every SM's two CTAs a few tiles to work
-// on, up to 256 (three halo rows and a row of dw per tile), down to 16.
+// Tokens per tile: the CTAs run in waves of two per SM, and a tile costs its tokens plus about 16
+// more (three halo tokens, filling the pipeline, a row of dw written and read).  The length with
+// the least waves x cost: 8192 tokens x 96 heads of 128 in one wave of 344 tokens take 150 us where
+// 64-token tiles (5.2 waves) took 182.
 int tile_of(int T, int Cn) {
-  int tile = 256;
-  while (tile > 16 && (long long)((T + tile - 1) / tile) * channel_blocks(Cn) < 8 * 148) tile /= 2;
-  // the grid's second dimension is limited to 65535
+  const long long blocks = channel_blocks(Cn), slots = 2 * 148;
+  long long best = 1LL << 60;
+  int tile = 4;
+  for (int t = 4; t <= 512; t += 4) {
+    const long long tiles = (T + t - 1) / t, cost = (blocks * tiles + slots - 1) / slots * (t + 16);
+    if (tiles <= 65535 && cost < best) {  // the grid's second dimension
+      best = cost;
+      tile = t;
+    }
+  }
   while ((T + (long long)tile - 1) / tile > 65535) tile *= 2;
   return tile;
 }
