@@ -20,9 +20,10 @@
 // dQ and dK of a key head's value heads are summed in registers in a fixed order.
 //
 // Per value head and chunk at D = 128 the reverse pass is 504 MMAs per warp (8 warps), the local
-// pass about 1000; both are bound by the mma.sync rate as the forward is.  The local pass keeps
-// S and dS' as split fp16 planes in shared memory (128 KB) with K, Q and U, one CTA per SM.
+// pass about 1000; a chunk of the local pass reads 270 KB.  The local pass keeps S and dS' as split
+// fp16 rows in shared memory (128 KB) with K, Q, U and dO or X, one persistent CTA per SM.
 #include "kda_gdr.cuh"
+#include "kda_tcgen05.cuh"
 
 namespace kda {
 namespace {
@@ -274,28 +275,51 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
 
 constexpr int kLocalThreads = 256;
 
+// A matrix of fp32 rows of D values becomes, in its place, one of split rows: per row D fp16 hi,
+// then D fp16 lo (4 D bytes as before), the 16-byte pieces of each XOR-swizzled by the row, so that
+// ldmatrix reads eight rows without bank conflicts.  A warp owns whole rows: no block barrier.
+template <int D> __device__ __forceinline__ uint32_t row_off(int row, int c8) {
+  return (uint32_t)(row * 4 * D + ((c8 ^ (row & 7)) << 4));
+}
+// B operand whose columns (n) are rows n0 .. n0 + 15; lo: the second term.
+template <int D>
+__device__ __forceinline__ void load_rows_b(uint32_t (&r)[4], uint32_t base, int n0, int k0, bool lo) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4(r, base + row_off<D>(n0 + (m >> 1) * 8 + (lane & 7), (k0 >> 3) + (m & 1)) + (lo ? 2 * D : 0));
+}
+// A operand of rows m0 .. m0 + 15.
+template <int D>
+__device__ __forceinline__ void load_rows_a(uint32_t (&r)[4], uint32_t base, int m0, int k0, bool lo) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4(r, base + row_off<D>(m0 + (m & 1) * 8 + (lane & 7), (k0 >> 3) + (m >> 1)) + (lo ? 2 * D : 0));
+}
+
 template <int D> struct LocalSmem {
   static constexpr uint32_t kK = 0, kQ = kQRows;
-  static constexpr uint32_t kSHi = kq_tile_bytes(D), kSLo = kSHi + D * D * 2;
-  static constexpr uint32_t kDHi = kSLo + D * D * 2, kDLo = kDHi + D * D * 2;
-  static constexpr uint32_t kU = kDLo + D * D * 2;          // U hi, lo; later W hi, lo, M hi, lo
-  static constexpr uint32_t kULo = kU + C * D * 2;
+  static constexpr uint32_t kS = kq_tile_bytes(D);   // S, D rows (key channels)
+  static constexpr uint32_t kD = kS + D * D * 4;     // dS'
+  static constexpr uint32_t kU = kD + D * D * 4;     // U, 64 rows; later W hi, lo, M hi, lo
   static constexpr uint32_t kUBytes = C * D * 4 > 4 * kTriBytes ? C * D * 4 : 4 * kTriBytes;
-  static constexpr uint32_t kSmall = kU + kUBytes;
+  static constexpr uint32_t kA = kU + kUBytes;       // dO, then X, 64 rows; later the sums
+  static constexpr uint32_t kSmall = kA + C * D * 4;
+  struct Sums {                        // in kA
+    float rows[2][C];                  // per half: what dgamma takes per row
+    float cols[4][C];                  // per row block: column sums
+    float tail[2][C], zk[2][C], db[2][C];
+    float cross[8];
+  };
   struct Small {
     alignas(16) float2 gamma[C];
-    float G[C], E[C], beta[C], us[C];  // us: scale of U's rows
-    float rows[2][C];                  // per half: sums that dgamma and dbeta take per row
-    float cols[4][C];                  // per row block: column sums
-    float tail[2][C], zk[2][C], db[2][C], xv[C];
-    float red[8][4];
+    float beta[C], us[C], as[C], xv[C];  // us, as: scales of U's and of dO's or X's rows
+    float red[8][2];
     float kq[2];
+    uint64_t states, rest;               // S and dS' have landed; U (and K and Q) have
   };
   static constexpr uint32_t kBytes = kSmall + sizeof(Small);
 };
 
 // The largest over the block of each of two values (one barrier pair).
-__device__ __forceinline__ float2 block_max2(float a, float b, float (*red)[4]) {
+__device__ __forceinline__ float2 block_max2(float a, float b, float (*red)[2]) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
@@ -315,6 +339,10 @@ __device__ __forceinline__ float2 block_max2(float a, float b, float (*red)[4]) 
   return make_float2(a, b);
 }
 
+__device__ __forceinline__ float max_abs4(const float4 &x, float m) {
+  return fmaxf(fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+}
+
 // Sum over the eight lanes that share accumulator columns.
 __device__ __forceinline__ float col_sum(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 4);
@@ -328,6 +356,8 @@ __device__ __forceinline__ float2 tile_pair(const uint8_t *tile, int row, int c8
   return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
+// Persistent: a CTA takes every gridDim.x-th (chunk, key head).  S and dS' of the next (chunk,
+// head) are fetched as soon as this one's have been used, behind the products that are left.
 template <typename Tin, int D>
 __global__ void __launch_bounds__(kLocalThreads, 1)
 gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
@@ -339,441 +369,483 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
   using Sm = LocalSmem<D>;
   constexpr int KK = D / 16;       // k-steps over the head dimension
   constexpr int NH = D / 16;       // 8-column blocks of a warp's half of the key channels
+  constexpr int LR = D / 4;        // lanes per row of an fp32 matrix
+  constexpr int RP = 32 / LR;      // rows per warp access
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sb = smem_addr(smem);
   typename Sm::Small &sm = *reinterpret_cast<typename Sm::Small *>(smem + Sm::kSmall);
+  typename Sm::Sums &sums = *reinterpret_cast<typename Sm::Sums *>(smem + Sm::kA);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int m = warp & 3, half = warp >> 2;       // token rows 16 m .., half of the columns
-  const int hk = blockIdx.x % HK;
-  const long long slot = blockIdx.x / HK;
-  int n, bos, eos, c;
-  if (!chunk_of_slot(cu, N, T, slot, status, n, bos, eos, c)) return;
-  if (!in_range(status, slot, slots(N, T))) return;
-  const int t0 = bos + c * C, len = min(C, eos - t0);
   const int r0 = 16 * m + lane / 4, r1 = r0 + 8, col = 2 * (lane & 3);
-
-  {
-    const uint8_t *kq = ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D);
-    cp_block(sb, kq, kq_tile_bytes(D));
-    cp_commit();
-    if (tid == 0) {
-      const float2 f = *reinterpret_cast<const float2 *>(kq + kq_tile_bytes(D));
-      sm.kq[0] = f.x;
-      sm.kq[1] = f.y;
-    }
-  }
-  float aq[NH][4], ak[NH][4];  // dQ, dK: rows r0, r1; columns 8 (half NH + i) + col
-  zero(aq);
-  zero(ak);
+  const int rl = lane / LR, cl = lane % LR;       // row and quad of a lane in a warp access
   const int group = HV / HK;
-  for (int j = 0; j < group; ++j) {
-    const int h = hk * group + j;
-    const size_t rec = (size_t)(slot * HV + h);
-    const float *Sg = reinterpret_cast<const float *>(ws + lay.state) + rec * D * D;
-    const float *Dg = reinterpret_cast<const float *>(ws + lay.dstate) + rec * D * D;
-    const float *Ug = reinterpret_cast<const float *>(ws + lay.u) + rec * C * D;
-    const float *Xg = reinterpret_cast<const float *>(ws + lay.x) + rec * C * D;
-    const float *vec = reinterpret_cast<const float *>(ws + lay.tp + rec * kTpBytes + kVec);
-    __syncthreads();  // the previous head has been read
-    if (tid < C) {
-      sm.G[tid] = vec[kVecG * C + tid];
-      sm.E[tid] = vec[kVecE * C + tid];
-      sm.beta[tid] = vec[kVecBeta * C + tid];
-    }
-    if (warp == 7) {
-      const float *g0 = g + (size_t)t0 * HV + h;
-      gamma_of(load_g(g0, HV, 2 * lane, len), load_g(g0, HV, 2 * lane + 1, len), sm.gamma);
-    }
-    // S and dS' as planes with one power of two per matrix; <dS', S> from the planes' values.
-    Scale ss, ds;
-    float cross = 0.f;
-    {
-      constexpr int kQuads = D * D / 4 / kLocalThreads;
-      float4 a[kQuads];
-      float big = 0.f;
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        a[i] = __ldg(reinterpret_cast<const float4 *>(Sg) + tid + i * kLocalThreads);
-        big = fmaxf(big, fmaxf(fmaxf(fabsf(a[i].x), fabsf(a[i].y)), fmaxf(fabsf(a[i].z), fabsf(a[i].w))));
-      }
-      ss = scale_of(block_max2(big, 0.f, sm.red).x);
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const int e = 4 * (tid + i * kLocalThreads), r = e / D, cc = e % D;
-        uint2 hi, lo;
-        split2(a[i].x, a[i].y, ss.inv, hi.x, lo.x);
-        split2(a[i].z, a[i].w, ss.inv, hi.y, lo.y);
-        const uint32_t at = tile_off<D>(r, cc >> 3) + 2 * (cc & 7);
-        *reinterpret_cast<uint2 *>(smem + Sm::kSHi + at) = hi;
-        *reinterpret_cast<uint2 *>(smem + Sm::kSLo + at) = lo;
-      }
-      big = 0.f;
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        a[i] = __ldg(reinterpret_cast<const float4 *>(Dg) + tid + i * kLocalThreads);
-        big = fmaxf(big, fmaxf(fmaxf(fabsf(a[i].x), fabsf(a[i].y)), fmaxf(fabsf(a[i].z), fabsf(a[i].w))));
-      }
-      ds = scale_of(block_max2(big, 0.f, sm.red).x);
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const int e = 4 * (tid + i * kLocalThreads), r = e / D, cc = e % D;
-        const uint32_t at = tile_off<D>(r, cc >> 3) + 2 * (cc & 7);
-        const uint2 sh = *reinterpret_cast<const uint2 *>(smem + Sm::kSHi + at);
-        const uint2 sl = *reinterpret_cast<const uint2 *>(smem + Sm::kSLo + at);
-        const float2 h0 = __half22float2(*reinterpret_cast<const __half2 *>(&sh.x));
-        const float2 h1 = __half22float2(*reinterpret_cast<const __half2 *>(&sh.y));
-        const float2 l0 = __half22float2(*reinterpret_cast<const __half2 *>(&sl.x));
-        const float2 l1 = __half22float2(*reinterpret_cast<const __half2 *>(&sl.y));
-        cross = fmaf(a[i].x, h0.x + l0.x, cross);
-        cross = fmaf(a[i].y, h0.y + l0.y, cross);
-        cross = fmaf(a[i].z, h1.x + l1.x, cross);
-        cross = fmaf(a[i].w, h1.y + l1.y, cross);
-        uint2 hi, lo;
-        split2(a[i].x, a[i].y, ds.inv, hi.x, lo.x);
-        split2(a[i].z, a[i].w, ds.inv, hi.y, lo.y);
-        *reinterpret_cast<uint2 *>(smem + Sm::kDHi + at) = hi;
-        *reinterpret_cast<uint2 *>(smem + Sm::kDLo + at) = lo;
-      }
-    }
-    {  // U: four threads per token row, a power of two per row
-      const int r = tid >> 2, part = tid & 3;
-      constexpr int kQuads = D / 16;
-      float4 a[kQuads];
-      float big = 0.f;
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        a[i] = __ldg(reinterpret_cast<const float4 *>(Ug + r * D) + part + 4 * i);
-        big = fmaxf(big, fmaxf(fmaxf(fabsf(a[i].x), fabsf(a[i].y)), fmaxf(fabsf(a[i].z), fabsf(a[i].w))));
-      }
-      const Scale us = scale_of(quad_max(big));
-#pragma unroll
-      for (int i = 0; i < kQuads; ++i) {
-        const int cc = 4 * (part + 4 * i);
-        uint2 hi, lo;
-        split2(a[i].x, a[i].y, us.inv, hi.x, lo.x);
-        split2(a[i].z, a[i].w, us.inv, hi.y, lo.y);
-        const uint32_t at = tile_off(r, cc >> 3) + 2 * (cc & 7);
-        *reinterpret_cast<uint2 *>(smem + Sm::kU + at) = hi;
-        *reinterpret_cast<uint2 *>(smem + Sm::kULo + at) = lo;
-      }
-      if (part == 0) sm.us[r] = us.s;
-    }
-    cp_wait<0>();
-    __syncthreads();
-    const float ks = sm.kq[0], qs = sm.kq[1];
+  const long long items = slots(N, T) * HK;
 
-    float dp[4][4], da[4][4];  // rows r0, r1; columns 32 half + 8 i + col
-    // A = dO~ or X (rows of this warp's tokens): z = A S^T, dp or da = A U^T.
-    auto rows_times = [&](const float *a0p, const float *a1p, bool ok0, bool ok1, float f,
-                          float (&z)[NH][4], float (&y)[4][4], float *dot, const Tin *v0, const Tin *v1) {
-      float a[2 * KK][4];  // columns 8 i + col of rows r0 (0, 1) and r1 (2, 3)
+  // The next item at or after `item` whose slot has a chunk; `items` if there is none.
+  int bos = 0, eos = 0, c = 0, n = 0;
+  auto next_item = [&](long long item) {
+    while (item < items &&
+           !(chunk_of_slot(cu, N, T, item / HK, status, n, bos, eos, c) &&
+             in_range(status, item / HK, slots(N, T))))
+      item += gridDim.x;
+    return item;
+  };
+  // One thread: S and dS' of a (chunk, head), 4 D^2 bytes each as the state passes left them.
+  auto fetch_states = [&](long long item, int j) {
+    const size_t rec = (size_t)(item / HK) * HV + item % HK * group + j;
+    tc::mbar_arrive_expect_tx(&sm.states, 2 * D * D * 4);
+    tc::bulk_load(smem + Sm::kS, ws + lay.state + rec * D * D * 4, D * D * 4, &sm.states);
+    tc::bulk_load(smem + Sm::kD, ws + lay.dstate + rec * D * D * 4, D * D * 4, &sm.states);
+  };
+  // Rows of a warp in place: `rows` rows from row0 on, in batches of four accesses.
+  auto split_rows = [&](uint32_t base, int row0, int rows, float inv) {
+#pragma unroll 1
+    for (int i = 0; i < rows; i += 4 * RP) {
+      float4 x[4];
 #pragma unroll
-      for (int i = 0; i < 2 * KK; ++i) {
-        float2 p = make_float2(0.f, 0.f), q = p;
-        if (ok0) p = *reinterpret_cast<const float2 *>(a0p + 8 * i + col);
-        if (ok1) q = *reinterpret_cast<const float2 *>(a1p + 8 * i + col);
-        a[i][0] = f * p.x; a[i][1] = f * p.y; a[i][2] = f * q.x; a[i][3] = f * q.y;
+      for (int k = 0; k < 4; ++k)
+        x[k] = *reinterpret_cast<const float4 *>(smem + base + (row0 + i + k * RP + rl) * 4 * D + 16 * cl);
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint2 hi, lo;
+        split2(x[k].x, x[k].y, inv, hi.x, lo.x);
+        split2(x[k].z, x[k].w, inv, hi.y, lo.y);
+        const uint32_t o = base + row_off<D>(row0 + i + k * RP + rl, cl >> 1) + 8 * (cl & 1);
+        *reinterpret_cast<uint2 *>(smem + o) = hi;
+        *reinterpret_cast<uint2 *>(smem + o + 2 * D) = lo;
       }
-      if (dot != nullptr) {  // X_r . V_r
-        float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * KK; ++i) {
-          if (ok0) d0 += a[i][0] * to_f32(v0[8 * i + col]) + a[i][1] * to_f32(v0[8 * i + col + 1]);
-          if (ok1) d1 += a[i][2] * to_f32(v1[8 * i + col]) + a[i][3] * to_f32(v1[8 * i + col + 1]);
-        }
-        d0 = quad_sum(d0);
-        d1 = quad_sum(d1);
-        if ((lane & 3) == 0) {
-          dot[r0] = d0;
-          dot[r1] = d1;
-        }
-      }
-      Scale s0, s1;
-      row_scales(a, s0, s1);
-      zero(z);
-      zero(y);
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        uint32_t hi[4], lo[4];
-        split_a(a, kk, s0, s1, hi, lo);
-#pragma unroll
-        for (int np = 0; np < NH / 2; ++np) {
-          uint32_t b[4], bl[4];
-          load_b<D>(b, sb + Sm::kSHi, half * (D / 2) + 16 * np, 16 * kk);
-          load_b<D>(bl, sb + Sm::kSLo, half * (D / 2) + 16 * np, 16 * kk);
-          mma(z[2 * np], hi, b[0], b[1]);
-          mma(z[2 * np + 1], hi, b[2], b[3]);
-          mma(z[2 * np], lo, b[0], b[1]);
-          mma(z[2 * np + 1], lo, b[2], b[3]);
-          mma(z[2 * np], hi, bl[0], bl[1]);
-          mma(z[2 * np + 1], hi, bl[2], bl[3]);
-        }
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-          if (2 * half + np > m) break;
-          uint32_t b[4], bl[4];
-          load_b(b, sb + Sm::kU, 32 * half + 16 * np, 16 * kk);
-          load_b(bl, sb + Sm::kULo, 32 * half + 16 * np, 16 * kk);
-          mma(y[2 * np], hi, b[0], b[1]);
-          mma(y[2 * np + 1], hi, b[2], b[3]);
-          mma(y[2 * np], lo, b[0], b[1]);
-          mma(y[2 * np + 1], lo, b[2], b[3]);
-          mma(y[2 * np], hi, bl[0], bl[1]);
-          mma(y[2 * np + 1], hi, bl[2], bl[3]);
-        }
-      }
-      const float f0 = s0.s * ss.s, f1 = s1.s * ss.s;
-#pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        z[i][0] *= f0; z[i][1] *= f0; z[i][2] *= f1; z[i][3] *= f1;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = *reinterpret_cast<const float2 *>(sm.us + 32 * half + 8 * i + col);
-        y[i][0] *= s0.s * u.x; y[i][1] *= s0.s * u.y;
-        y[i][2] *= s1.s * u.x; y[i][3] *= s1.s * u.y;
-      }
-    };
-    // Row dots of z with the rows of a tile (keys or queries), summed over this warp's columns.
-    auto row_dots = [&](const float (&z)[NH][4], uint32_t tile, float f, float &d0, float &d1) {
-      d0 = d1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        const float2 a = tile_pair(smem + tile, r0, half * NH + i, col);
-        const float2 b = tile_pair(smem + tile, r1, half * NH + i, col);
-        d0 += z[i][0] * a.x + z[i][1] * a.y;
-        d1 += z[i][2] * b.x + z[i][3] * b.y;
-      }
-      d0 = f * quad_sum(d0);
-      d1 = f * quad_sum(d1);
-    };
-    float rg0, rg1;  // what dgamma takes per row
-    float z[NH][4];
-    const float g0 = sm.G[r0], g1 = sm.G[r1], b0 = sm.beta[r0], b1 = sm.beta[r1];
-    {
-      const float *p = d_o + ((size_t)t0 * HV + h) * D;
-      rows_times(p + (size_t)r0 * HV * D, p + (size_t)r1 * HV * D, r0 < len, r1 < len, scale, z, dp,
-                 nullptr, nullptr, nullptr);
-#pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        z[i][0] *= g0; z[i][1] *= g0; z[i][2] *= g1; z[i][3] *= g1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) aq[i][e] += z[i][e];
-      }
-      row_dots(z, Sm::kQ, qs, rg0, rg1);
+      __syncwarp();
     }
-    {
-      const Tin *vp = v + ((size_t)t0 * HV + h) * D;
-      rows_times(Xg + r0 * D, Xg + r1 * D, r0 < len, r1 < len, 1.f, z, da, half == 0 ? sm.xv : nullptr,
-                 vp + (size_t)r0 * HV * D, vp + (size_t)r1 * HV * D);
-      float d0, d1;
-      row_dots(z, Sm::kK, ks, d0, d1);
-      if ((lane & 3) == 0) {
-        sm.zk[half][r0] = d0;
-        sm.zk[half][r1] = d1;
-      }
-      const float f0 = g0 * b0, f1 = g1 * b1;
-      rg0 -= f0 * d0;
-      rg1 -= f1 * d1;
+  };
+  // A warp's 8 of 64 rows, held in registers, with a scale per row.
+  constexpr int kHeld = 8 / RP;
+  auto store_rows = [&](const float4 (&x)[kHeld], uint32_t base, float *scales) {
 #pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        ak[i][0] -= f0 * z[i][0]; ak[i][1] -= f0 * z[i][1];
-        ak[i][2] -= f1 * z[i][2]; ak[i][3] -= f1 * z[i][3];
-      }
+    for (int k = 0; k < kHeld; ++k) {
+      const int row = 8 * warp + k * RP + rl;
+      float big = max_abs4(x[k], 0.f);
+#pragma unroll
+      for (int off = LR / 2; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+      const Scale s = scale_of(big);
+      uint2 hi, lo;
+      split2(x[k].x, x[k].y, s.inv, hi.x, lo.x);
+      split2(x[k].z, x[k].w, s.inv, hi.y, lo.y);
+      const uint32_t o = base + row_off<D>(row, cl >> 1) + 8 * (cl & 1);
+      *reinterpret_cast<uint2 *>(smem + o) = hi;
+      *reinterpret_cast<uint2 *>(smem + o + 2 * D) = lo;
+      if (cl == 0) scales[row] = s.s;
     }
-    {  // E U dS'^T
-      zero(z);
+  };
+  // The same for rows that lie in their place as fp32.
+  auto split_own = [&](uint32_t base, float *scales) {
+    float4 x[kHeld];
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        uint32_t hi[4], lo[4];
-        load_a(hi, sb + Sm::kU, 16 * m, 16 * kk);
-        load_a(lo, sb + Sm::kULo, 16 * m, 16 * kk);
-#pragma unroll
-        for (int np = 0; np < NH / 2; ++np) {
-          uint32_t b[4], bl[4];
-          load_b<D>(b, sb + Sm::kDHi, half * (D / 2) + 16 * np, 16 * kk);
-          load_b<D>(bl, sb + Sm::kDLo, half * (D / 2) + 16 * np, 16 * kk);
-          mma(z[2 * np], hi, b[0], b[1]);
-          mma(z[2 * np + 1], hi, b[2], b[3]);
-          mma(z[2 * np], lo, b[0], b[1]);
-          mma(z[2 * np + 1], lo, b[2], b[3]);
-          mma(z[2 * np], hi, bl[0], bl[1]);
-          mma(z[2 * np + 1], hi, bl[2], bl[3]);
+    for (int k = 0; k < kHeld; ++k)
+      x[k] = *reinterpret_cast<const float4 *>(smem + base + (8 * warp + k * RP + rl) * 4 * D + 16 * cl);
+    __syncwarp();
+    store_rows(x, base, scales);
+  };
+
+  if (tid == 0) {
+    tc::mbar_init(&sm.states, 1);
+    tc::mbar_init(&sm.rest, 1);
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  uint32_t par = 0;  // of both barriers: one phase each per (chunk, head)
+  long long item = next_item(blockIdx.x);
+  if (tid == 0 && item < items) fetch_states(item, 0);
+  while (item < items) {
+    const long long slot = item / HK;
+    const int hk = (int)(item % HK);
+    const int t0 = bos + c * C, len = min(C, eos - t0);
+    float aq[NH][4], ak[NH][4];  // dQ, dK: rows r0, r1; columns 8 (half NH + i) + col
+    zero(aq);
+    zero(ak);
+    long long following = items;
+    for (int j = 0; j < group; ++j) {
+      const int h = hk * group + j;
+      const size_t rec = (size_t)(slot * HV + h);
+      const float *Ug = reinterpret_cast<const float *>(ws + lay.u) + rec * C * D;
+      const float *Xg = reinterpret_cast<const float *>(ws + lay.x) + rec * C * D;
+      const float *Og = d_o + ((size_t)t0 * HV + h) * D;
+      // U (with the first head K and Q) and dO on their way behind S and dS'.
+      if (tid == 0) {
+        const uint8_t *kq = ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D);
+        tc::mbar_arrive_expect_tx(&sm.rest, C * D * 4 + (j == 0 ? kq_tile_bytes(D) : 0));
+        tc::bulk_load(smem + Sm::kU, Ug, C * D * 4, &sm.rest);
+        if (j == 0) {
+          tc::bulk_load(smem, kq, kq_tile_bytes(D), &sm.rest);
+          const float2 f = *reinterpret_cast<const float2 *>(kq + kq_tile_bytes(D));
+          sm.kq[0] = f.x;
+          sm.kq[1] = f.y;
         }
       }
-      const float f0 = sm.us[r0] * ds.s * sm.E[r0], f1 = sm.us[r1] * ds.s * sm.E[r1];
 #pragma unroll
-      for (int i = 0; i < NH; ++i) {
-        z[i][0] *= f0; z[i][1] *= f0; z[i][2] *= f1; z[i][3] *= f1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ak[i][e] += z[i][e];
+      for (int k = 0; k < kHeld; ++k) {
+        const int row = 8 * warp + k * RP + rl;
+        cp16(sb + Sm::kA + row * 4 * D + 16 * cl, Og + (size_t)min(row, len - 1) * HV * D + 4 * cl, row < len);
       }
-      float d0, d1;
-      row_dots(z, Sm::kK, ks, d0, d1);
-      if ((lane & 3) == 0) {
-        sm.tail[half][r0] = d0;
-        sm.tail[half][r1] = d1;
-      }
-    }
-    // W, M and their sums over rows and columns; Q K^T and K K^T again, from the tiles.  A token's
-    // own term decays by nothing: it stays out of the sums, where it would be added and taken
-    // away again, next to which the others may be small.
-    float bigw = 0.f, bigm = 0.f;
-    {
-      float qk[4][4], kk2[4][4];
-      zero(qk);
-      zero(kk2);
+      cp_commit();
+      if (warp == 7) {
+        const float *g0 = g + (size_t)t0 * HV + h;
+        gamma_of(load_g(g0, HV, 2 * lane, len), load_g(g0, HV, 2 * lane + 1, len), sm.gamma);
+      } else if (warp == 6) {
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        uint32_t a[4], aa[4];
-        load_a<kKq>(a, sb + Sm::kQ, 16 * m, 16 * kk);
-        load_a<kKq>(aa, sb + Sm::kK, 16 * m, 16 * kk);
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-          if (2 * half + np > m) break;
-          uint32_t b[4];
-          load_b<kKq>(b, sb + Sm::kK, 32 * half + 16 * np, 16 * kk);
-          mma(qk[2 * np], a, b[0], b[1]);
-          mma(qk[2 * np + 1], a, b[2], b[3]);
-          mma(kk2[2 * np], aa, b[0], b[1]);
-          mma(kk2[2 * np + 1], aa, b[2], b[3]);
+        for (int i = 0; i < 2; ++i) {
+          const int t = lane + 32 * i;
+          sm.beta[t] = t < len ? __ldg(beta + (size_t)(t0 + t) * HV + h) : 0.f;
         }
       }
+      // S and dS' with one power of two per matrix, and <dS', S>.
+      if (!tc::wait_all(&sm.states, par, status)) {
+        if (tid == 0) {  // what is in flight lands before the CTA's memory goes
+          tc::drain(&sm.states);
+          tc::drain(&sm.rest);
+        }
+        cp_wait<0>();
+        __syncthreads();
+        return;
+      }
+      float cross = 0.f;
+      float2 big = make_float2(0.f, 0.f);
+      constexpr int kRows = D / 8;  // of each matrix per warp
+#pragma unroll 4
+      for (int i = 0; i < kRows; i += RP) {
+        const uint32_t o = (kRows * warp + i + rl) * 4 * D + 16 * cl;
+        const float4 a = *reinterpret_cast<const float4 *>(smem + Sm::kS + o);
+        const float4 b = *reinterpret_cast<const float4 *>(smem + Sm::kD + o);
+        big.x = max_abs4(a, big.x);
+        big.y = max_abs4(b, big.y);
+        cross += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+      }
+      big = block_max2(big.x, big.y, sm.red);
+      const Scale ss = scale_of(big.x), ds = scale_of(big.y);
+      split_rows(Sm::kS, kRows * warp, kRows, ss.inv);
+      split_rows(Sm::kD, kRows * warp, kRows, ds.inv);
+      cp_wait<0>();  // this thread's part of its own warp's rows of dO
+      __syncwarp();
+      split_own(Sm::kA, sm.as);
+      if (!tc::wait_all(&sm.rest, par, status)) {
+        if (tid == 0) tc::drain(&sm.rest);
+        __syncthreads();
+        return;
+      }
+      split_own(Sm::kU, sm.us);
+      __syncthreads();
+      par ^= 1;
+      // X and V, on their way behind the first products.
+      float4 x[kHeld];
+      uint2 vx[kHeld];
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int row = 8 * warp + k * RP + rl;
+        x[k] = __ldg(reinterpret_cast<const float4 *>(Xg + row * D) + cl);
+        vx[k] = make_uint2(0u, 0u);
+        if (row < len)
+          vx[k] = __ldg(reinterpret_cast<const uint2 *>(v + ((size_t)(t0 + row) * HV + h) * D) + cl);
+      }
+      const float ks = sm.kq[0], qs = sm.kq[1];
+
+      float dp[4][4], da[4][4];  // rows r0, r1; columns 32 half + 8 i + col
+      // z = (a matrix of 64 rows) (a matrix of key channels)^T, this warp's rows and columns, and
+      // with_u: y = the same 64 rows times U^T, in the blocks that reach below the diagonal.
+      auto rows_times = [&](uint32_t a, uint32_t b, float (&z)[NH][4], float (&y)[4][4], bool with_u) {
+        zero(z);
+        if (with_u) zero(y);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+          uint32_t hi[4], lo[4];
+          load_rows_a<D>(hi, sb + a, 16 * m, 16 * kk, false);
+          load_rows_a<D>(lo, sb + a, 16 * m, 16 * kk, true);
+#pragma unroll
+          for (int np = 0; np < NH / 2; ++np) {
+            uint32_t bh[4], bl[4];
+            load_rows_b<D>(bh, sb + b, half * (D / 2) + 16 * np, 16 * kk, false);
+            load_rows_b<D>(bl, sb + b, half * (D / 2) + 16 * np, 16 * kk, true);
+            mma(z[2 * np], hi, bh[0], bh[1]);
+            mma(z[2 * np + 1], hi, bh[2], bh[3]);
+            mma(z[2 * np], lo, bh[0], bh[1]);
+            mma(z[2 * np + 1], lo, bh[2], bh[3]);
+            mma(z[2 * np], hi, bl[0], bl[1]);
+            mma(z[2 * np + 1], hi, bl[2], bl[3]);
+          }
+          if (!with_u) continue;
+#pragma unroll
+          for (int np = 0; np < 2; ++np) {
+            if (2 * half + np > m) break;
+            uint32_t bh[4], bl[4];
+            load_rows_b<D>(bh, sb + Sm::kU, 32 * half + 16 * np, 16 * kk, false);
+            load_rows_b<D>(bl, sb + Sm::kU, 32 * half + 16 * np, 16 * kk, true);
+            mma(y[2 * np], hi, bh[0], bh[1]);
+            mma(y[2 * np + 1], hi, bh[2], bh[3]);
+            mma(y[2 * np], lo, bh[0], bh[1]);
+            mma(y[2 * np + 1], lo, bh[2], bh[3]);
+            mma(y[2 * np], hi, bl[0], bl[1]);
+            mma(y[2 * np + 1], hi, bl[2], bl[3]);
+          }
+        }
+      };
+      auto scale_y = [&](float (&y)[4][4], float f0, float f1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 u = *reinterpret_cast<const float2 *>(sm.us + 32 * half + 8 * i + col);
+          y[i][0] *= f0 * u.x; y[i][1] *= f0 * u.y;
+          y[i][2] *= f1 * u.x; y[i][3] *= f1 * u.y;
+        }
+      };
+      // Row dots of z with the rows of a tile (keys or queries), summed over this warp's columns.
+      auto row_dots = [&](const float (&z)[NH][4], uint32_t tile, float f, float &d0, float &d1) {
+        d0 = d1 = 0.f;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          const float2 a = tile_pair(smem + tile, r0, half * NH + i, col);
+          const float2 b = tile_pair(smem + tile, r1, half * NH + i, col);
+          d0 += z[i][0] * a.x + z[i][1] * a.y;
+          d1 += z[i][2] * b.x + z[i][3] * b.y;
+        }
+        d0 = f * quad_sum(d0);
+        d1 = f * quad_sum(d1);
+      };
+      float z[NH][4];
+      float rg0, rg1, zk0, zk1, tl0, tl1;
       const float2 gr[2] = {sm.gamma[r0], sm.gamma[r1]};
-      float nb[2] = {0.f, 0.f}, rows[2] = {0.f, 0.f};
+      const float g0 = ex2_approx(gr[0].x + gr[0].y), g1 = ex2_approx(gr[1].x + gr[1].y);
+      const float b0 = sm.beta[r0], b1 = sm.beta[r1];
+      {  // dO~ S^T and dO~ U^T
+        rows_times(Sm::kA, Sm::kS, z, dp, true);
+        const float f0 = scale * sm.as[r0], f1 = scale * sm.as[r1];
+        scale_y(dp, f0, f1);
+        const float z0 = g0 * f0 * ss.s, z1 = g1 * f1 * ss.s;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float cs[2] = {0.f, 0.f};
+        for (int i = 0; i < NH; ++i) {
+          z[i][0] *= z0; z[i][1] *= z0; z[i][2] *= z1; z[i][3] *= z1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = e >> 1 ? r1 : r0, cc = 32 * half + 8 * i + col + (e & 1);
-          const float dec = cc <= r ? decay_between(gr[e >> 1], sm.gamma[cc]) : 0.f;
-          const float w = cc <= r ? dp[i][e] * dec : 0.f;
-          const float m0 = cc < r ? -da[i][e] * dec : 0.f;  // dA D
-          const float mk = m0 * (ks * ks * kk2[i][e]);
-          const float b = e >> 1 ? b1 : b0;
-          const float x = cc < r ? w * (qs * ks * qk[i][e]) + b * mk : 0.f;
-          nb[e >> 1] += mk;
-          rows[e >> 1] += x;
-          cs[e & 1] += x;
-          dp[i][e] = w;
-          da[i][e] = b * m0;
-          bigw = fmaxf(bigw, fabsf(w));
-          bigm = fmaxf(bigm, fabsf(da[i][e]));
+          for (int e = 0; e < 4; ++e) aq[i][e] += z[i][e];
         }
+        row_dots(z, Sm::kQ, qs, rg0, rg1);
+      }
+      __syncthreads();
+      // X's rows, and X_r . V_r on the way.
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int row = 8 * warp + k * RP + rl;
+        const Tin *vp = reinterpret_cast<const Tin *>(&vx[k]);
+        float d = x[k].x * to_f32(vp[0]) + x[k].y * to_f32(vp[1]) + x[k].z * to_f32(vp[2]) +
+                  x[k].w * to_f32(vp[3]);
+#pragma unroll
+        for (int off = LR / 2; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+        if (cl == 0) sm.xv[row] = d;
+      }
+      store_rows(x, Sm::kA, sm.as);
+      __syncthreads();
+      {  // X S^T and X U^T
+        rows_times(Sm::kA, Sm::kS, z, da, true);
+        const float f0 = sm.as[r0], f1 = sm.as[r1];
+        scale_y(da, f0, f1);
+        const float z0 = f0 * ss.s, z1 = f1 * ss.s;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          z[i][0] *= z0; z[i][1] *= z0; z[i][2] *= z1; z[i][3] *= z1;
+        }
+        row_dots(z, Sm::kK, ks, zk0, zk1);
+        const float k0 = g0 * b0, k1 = g1 * b1;
+        rg0 -= k0 * zk0;
+        rg1 -= k1 * zk1;
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          ak[i][0] -= k0 * z[i][0]; ak[i][1] -= k0 * z[i][1];
+          ak[i][2] -= k1 * z[i][2]; ak[i][3] -= k1 * z[i][3];
+        }
+      }
+      {  // E U dS'^T
+        rows_times(Sm::kU, Sm::kD, z, da, false);
+        const float2 gl = sm.gamma[C - 1];
+        const float f0 = sm.us[r0] * ds.s * decay_between(gl, gr[0]);
+        const float f1 = sm.us[r1] * ds.s * decay_between(gl, gr[1]);
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          z[i][0] *= f0; z[i][1] *= f0; z[i][2] *= f1; z[i][3] *= f1;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ak[i][e] += z[i][e];
+        }
+        row_dots(z, Sm::kK, ks, tl0, tl1);
+      }
+      // W, M and their sums over rows and columns; Q K^T and K K^T again, from the tiles.  A token's
+      // own term decays by nothing: it stays out of the sums, where it would be added and taken
+      // away again, next to which the others may be small.
+      float bigw = 0.f, bigm = 0.f, cs[4][2], nb[2] = {0.f, 0.f};
+      {
+        float qk[4][4], kk2[4][4];
+        zero(qk);
+        zero(kk2);
+#pragma unroll
+        for (int kk = 0; kk < KK; ++kk) {
+          uint32_t a[4], aa[4];
+          load_a<kKq>(a, sb + Sm::kQ, 16 * m, 16 * kk);
+          load_a<kKq>(aa, sb + Sm::kK, 16 * m, 16 * kk);
+#pragma unroll
+          for (int np = 0; np < 2; ++np) {
+            if (2 * half + np > m) break;
+            uint32_t b[4];
+            load_b<kKq>(b, sb + Sm::kK, 32 * half + 16 * np, 16 * kk);
+            mma(qk[2 * np], a, b[0], b[1]);
+            mma(qk[2 * np + 1], a, b[2], b[3]);
+            mma(kk2[2 * np], aa, b[0], b[1]);
+            mma(kk2[2 * np + 1], aa, b[2], b[3]);
+          }
+        }
+        float rows[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cs[i][0] = cs[i][1] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = e >> 1 ? r1 : r0, cc = 32 * half + 8 * i + col + (e & 1);
+            const float dec = cc <= r ? decay_between(gr[e >> 1], sm.gamma[cc]) : 0.f;
+            const float w = cc <= r ? dp[i][e] * dec : 0.f;
+            const float m0 = cc < r ? -da[i][e] * dec : 0.f;  // dA D
+            const float mk = m0 * (ks * ks * kk2[i][e]);
+            const float b = e >> 1 ? b1 : b0;
+            const float t = cc < r ? w * (qs * ks * qk[i][e]) + b * mk : 0.f;
+            nb[e >> 1] += mk;
+            rows[e >> 1] += t;
+            cs[i][e & 1] += t;
+            dp[i][e] = w;
+            da[i][e] = b * m0;
+            bigw = fmaxf(bigw, fabsf(w));
+            bigm = fmaxf(bigm, fabsf(da[i][e]));
+          }
+          cs[i][0] = col_sum(cs[i][0]);
+          cs[i][1] = col_sum(cs[i][1]);
+        }
+        rg0 += quad_sum(rows[0]);
+        rg1 += quad_sum(rows[1]);
+        nb[0] = quad_sum(nb[0]);
+        nb[1] = quad_sum(nb[1]);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, off);
+      tc::fence_async_smem();  // the split rows were ordinary writes; the copies below are not
+      const float2 most = block_max2(bigw, bigm, sm.red);  // also: S, dS', U, X have been read
+      if (j + 1 < group) {
+        if (tid == 0) fetch_states(item, j + 1);
+      } else {
+        following = next_item(item + gridDim.x);  // bos, eos and c are the next item's from here on
+        if (tid == 0 && following < items) fetch_states(following, 0);
+      }
+      const Scale sw = scale_of(most.x), sn = scale_of(most.y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float t = col_sum(cs[e]);
-          if (lane < 4) sm.cols[m][32 * half + 8 * i + col + e] = t;
+          const uint32_t at = tile_off(e ? r1 : r0, 4 * half + i) + 2 * col;
+          uint32_t hi, lo;
+          split2(dp[i][2 * e], dp[i][2 * e + 1], sw.inv, hi, lo);
+          *reinterpret_cast<uint32_t *>(smem + Sm::kU + at) = hi;
+          *reinterpret_cast<uint32_t *>(smem + Sm::kU + kTriBytes + at) = lo;
+          split2(da[i][2 * e], da[i][2 * e + 1], sn.inv, hi, lo);
+          *reinterpret_cast<uint32_t *>(smem + Sm::kU + 2 * kTriBytes + at) = hi;
+          *reinterpret_cast<uint32_t *>(smem + Sm::kU + 3 * kTriBytes + at) = lo;
+          if (lane < 4) sums.cols[m][32 * half + 8 * i + col + e] = cs[i][e];
         }
-      }
-      rg0 += quad_sum(rows[0]);
-      rg1 += quad_sum(rows[1]);
-      nb[0] = quad_sum(nb[0]);
-      nb[1] = quad_sum(nb[1]);
       if ((lane & 3) == 0) {
-        sm.rows[half][r0] = rg0;
-        sm.rows[half][r1] = rg1;
-        sm.db[half][r0] = nb[0];
-        sm.db[half][r1] = nb[1];
+        sums.rows[half][r0] = rg0;
+        sums.rows[half][r1] = rg1;
+        sums.zk[half][r0] = zk0;
+        sums.zk[half][r1] = zk1;
+        sums.tail[half][r0] = tl0;
+        sums.tail[half][r1] = tl1;
+        sums.db[half][r0] = nb[0];
+        sums.db[half][r1] = nb[1];
       }
-    }
-    const float2 big = block_max2(bigw, bigm, sm.red);  // also: U has been read
-    const Scale sw = scale_of(big.x), sn = scale_of(big.y);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t at = tile_off(e ? r1 : r0, 4 * half + i) + 2 * col;
-        uint32_t hi, lo;
-        split2(dp[i][2 * e], dp[i][2 * e + 1], sw.inv, hi, lo);
-        *reinterpret_cast<uint32_t *>(smem + Sm::kU + at) = hi;
-        *reinterpret_cast<uint32_t *>(smem + Sm::kU + kTriBytes + at) = lo;
-        split2(da[i][2 * e], da[i][2 * e + 1], sn.inv, hi, lo);
-        *reinterpret_cast<uint32_t *>(smem + Sm::kU + 2 * kTriBytes + at) = hi;
-        *reinterpret_cast<uint32_t *>(smem + Sm::kU + 3 * kTriBytes + at) = lo;
-      }
-    // <dS', S>, summed in a fixed order
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, off);
-    if (lane == 0) sm.red[warp][2] = cross;
-    __syncthreads();
+      if (lane == 0) sums.cross[warp] = cross;
+      __syncthreads();
 
-    auto times = [&](uint32_t plane, bool transposed, uint32_t tile, float f, float (&out)[NH][4]) {
-      zero(z);
+      auto times = [&](uint32_t plane, bool transposed, uint32_t tile, float f, float (&out)[NH][4]) {
+        zero(z);
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        if (transposed ? kk < m : kk > m) continue;
-        uint32_t hi[4], lo[4];
-        if (transposed) {
-          load_at(hi, plane, 16 * m, 16 * kk);
-          load_at(lo, plane + kTriBytes, 16 * m, 16 * kk);
-        } else {
-          load_a(hi, plane, 16 * m, 16 * kk);
-          load_a(lo, plane + kTriBytes, 16 * m, 16 * kk);
+        for (int kk = 0; kk < 4; ++kk) {
+          if (transposed ? kk < m : kk > m) continue;
+          uint32_t hi[4], lo[4];
+          if (transposed) {
+            load_at(hi, plane, 16 * m, 16 * kk);
+            load_at(lo, plane + kTriBytes, 16 * m, 16 * kk);
+          } else {
+            load_a(hi, plane, 16 * m, 16 * kk);
+            load_a(lo, plane + kTriBytes, 16 * m, 16 * kk);
+          }
+#pragma unroll
+          for (int np = 0; np < NH / 2; ++np) {
+            uint32_t b[4];
+            load_bt<kKq>(b, tile, half * (D / 2) + 16 * np, 16 * kk);
+            mma(z[2 * np], hi, b[0], b[1]);
+            mma(z[2 * np + 1], hi, b[2], b[3]);
+            mma(z[2 * np], lo, b[0], b[1]);
+            mma(z[2 * np + 1], lo, b[2], b[3]);
+          }
         }
 #pragma unroll
-        for (int np = 0; np < NH / 2; ++np) {
-          uint32_t b[4];
-          load_bt<kKq>(b, tile, half * (D / 2) + 16 * np, 16 * kk);
-          mma(z[2 * np], hi, b[0], b[1]);
-          mma(z[2 * np + 1], hi, b[2], b[3]);
-          mma(z[2 * np], lo, b[0], b[1]);
-          mma(z[2 * np + 1], lo, b[2], b[3]);
-        }
-      }
+        for (int i = 0; i < NH; ++i)
 #pragma unroll
-      for (int i = 0; i < NH; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) out[i][e] = fmaf(f, z[i][e], out[i][e]);
-    };
-    times(sb + Sm::kU, false, sb + Sm::kK, sw.s * ks, aq);
-    times(sb + Sm::kU, true, sb + Sm::kQ, sw.s * qs, ak);
-    times(sb + Sm::kU + 2 * kTriBytes, false, sb + Sm::kK, sn.s * ks, ak);
-    times(sb + Sm::kU + 2 * kTriBytes, true, sb + Sm::kK, sn.s * ks, ak);
+          for (int e = 0; e < 4; ++e) out[i][e] = fmaf(f, z[i][e], out[i][e]);
+      };
+      times(sb + Sm::kU, false, sb + Sm::kK, sw.s * ks, aq);
+      times(sb + Sm::kU, true, sb + Sm::kQ, sw.s * qs, ak);
+      times(sb + Sm::kU + 2 * kTriBytes, false, sb + Sm::kK, sn.s * ks, ak);
+      times(sb + Sm::kU + 2 * kTriBytes, true, sb + Sm::kK, sn.s * ks, ak);
 
-    if (warp == 0) {  // dg and dbeta of tokens 2 lane, 2 lane + 1
-      double d[2], e = 0.0;
+      if (warp == 0) {  // dg and dbeta of tokens 2 lane, 2 lane + 1
+        double d[2], e = 0.0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 2 * lane + i;
-        // M's contribution to dbeta has beta left out, so that it holds for beta = 0 too.
-        const float b = sm.xv[r] - sm.G[r] * (sm.zk[0][r] + sm.zk[1][r]) + sm.db[0][r] + sm.db[1][r];
-        if (r < len) dbeta[(size_t)(t0 + r) * HV + h] = b;
-        const double et = (double)sm.tail[0][r] + sm.tail[1][r];
-        d[i] = (double)sm.rows[0][r] + sm.rows[1][r] - et -
-               ((double)sm.cols[0][r] + sm.cols[1][r] + sm.cols[2][r] + sm.cols[3][r]);
-        e += et;
+        for (int i = 0; i < 2; ++i) {
+          const int r = 2 * lane + i;
+          const float2 gm = sm.gamma[r];
+          // M's contribution to dbeta has beta left out, so that it holds for beta = 0 too.
+          const float b = sm.xv[r] - ex2_approx(gm.x + gm.y) * (sums.zk[0][r] + sums.zk[1][r]) +
+                          sums.db[0][r] + sums.db[1][r];
+          if (r < len) dbeta[(size_t)(t0 + r) * HV + h] = b;
+          const double et = (double)sums.tail[0][r] + sums.tail[1][r];
+          d[i] = (double)sums.rows[0][r] + sums.rows[1][r] - et -
+                 ((double)sums.cols[0][r] + sums.cols[1][r] + sums.cols[2][r] + sums.cols[3][r]);
+          e += et;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += sums.cross[i];
+        const float2 gl = sm.gamma[C - 1];
+        if (lane == 31) d[1] += e + (double)(ex2_approx(gl.x + gl.y) * t);
+        double s = d[0] + d[1];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const double o = __shfl_down_sync(0xffffffffu, s, off);
+          if (lane + off < 32) s += o;
+        }
+        if (2 * lane < len) dg[(size_t)(t0 + 2 * lane) * HV + h] = (float)s;
+        if (2 * lane + 1 < len) dg[(size_t)(t0 + 2 * lane + 1) * HV + h] = (float)(s - d[0]);
       }
+      tc::fence_async_smem();
+      __syncthreads();  // gamma, the sums, W and M (and K and Q, after the last head) have been read
+    }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
-      float x = 0.f;
+    for (int e = 0; e < 2; ++e) {
+      const int r = e ? r1 : r0;
+      if (r >= len) continue;
+      const size_t at = ((size_t)(t0 + r) * HK + hk) * D + half * (D / 2) + col;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x += sm.red[i][2];
-      if (lane == 31) d[1] += e + (double)(sm.G[C - 1] * (x * ss.s));
-      double s = d[0] + d[1];
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const double o = __shfl_down_sync(0xffffffffu, s, off);
-        if (lane + off < 32) s += o;
+      for (int i = 0; i < NH; ++i) {
+        Tin o[2] = {from_f32<Tin>(aq[i][2 * e]), from_f32<Tin>(aq[i][2 * e + 1])};
+        *reinterpret_cast<uint32_t *>(dq + at + 8 * i) = *reinterpret_cast<const uint32_t *>(o);
+        o[0] = from_f32<Tin>(ak[i][2 * e]);
+        o[1] = from_f32<Tin>(ak[i][2 * e + 1]);
+        *reinterpret_cast<uint32_t *>(dk + at + 8 * i) = *reinterpret_cast<const uint32_t *>(o);
       }
-      if (2 * lane < len) dg[(size_t)(t0 + 2 * lane) * HV + h] = (float)s;
-      if (2 * lane + 1 < len) dg[(size_t)(t0 + 2 * lane + 1) * HV + h] = (float)(s - d[0]);
     }
-  }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = e ? r1 : r0;
-    if (r >= len) continue;
-    const size_t at = ((size_t)(t0 + r) * HK + hk) * D + half * (D / 2) + col;
-#pragma unroll
-    for (int i = 0; i < NH; ++i) {
-      Tin o[2] = {from_f32<Tin>(aq[i][2 * e]), from_f32<Tin>(aq[i][2 * e + 1])};
-      *reinterpret_cast<uint32_t *>(dq + at + 8 * i) = *reinterpret_cast<const uint32_t *>(o);
-      o[0] = from_f32<Tin>(ak[i][2 * e]);
-      o[1] = from_f32<Tin>(ak[i][2 * e + 1]);
-      *reinterpret_cast<uint32_t *>(dk + at + 8 * i) = *reinterpret_cast<const uint32_t *>(o);
-    }
+    item = following;
   }
 }
 
@@ -811,9 +883,9 @@ cudaError_t launch_typed(const void *v, const float *g, const float *beta, const
   const int bytes = (int)LocalSmem<D>::kBytes;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const long long ctas = slots(N, T) * HK;
-  if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
-  kern<<<(unsigned)ctas, kLocalThreads, bytes, s>>>(
+  const long long items = slots(N, T) * HK;
+  const unsigned ctas = (unsigned)(items < 148 ? items : 148);  // one per SM
+  kern<<<ctas, kLocalThreads, bytes, s>>>(
       static_cast<const Tin *>(v), g, beta, d_o, cu, scale, N, T, HK, HV,
       static_cast<const uint8_t *>(ws), layout(N, T, HK, HV, D, true), static_cast<Tin *>(dq),
       static_cast<Tin *>(dk), dg, dbeta, status);
