@@ -649,15 +649,18 @@ def kda_output_epilogue(o, gate, weight, out, *, eps: float = 1e-5, stream=None)
 
 # ---- gated delta rule with one decay per head; backward of prologue and epilogue ----------
 # These functions check shapes as well: the kernels trust the sizes they are given.  A decode
-# step's kernel takes a few microseconds, so the checks are written to cost little when they
-# pass: one expression per tensor, pointers handed over as plain integers.
+# step's kernel takes three microseconds, so a call's checks are one expression that reads each
+# attribute once; where it fails, _p looks at the tensors one by one and names what is wrong.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _refuse(t, name, shape, dtype, device):
-    """The error for a tensor that is not a contiguous one of this shape and dtype on CUDA
-    device number ``device``."""
+def _p(t, name, shape, dtype, device):
+    """Address of a contiguous tensor of this shape and dtype on CUDA device number ``device``,
+    the current one (None: None); anything else is an error that says why."""
+    if t is None:
+        return None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != device:
@@ -666,16 +669,8 @@ def _refuse(t, name, shape, dtype, device):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _p(t, name, shape, dtype, device):
-    """Address of a contiguous tensor of this shape and dtype on the current device (None: 0)."""
-    if t is None:
-        return None
-    if (t.shape != shape or t.dtype is not dtype or t.get_device() != device
-            or not t.is_contiguous()):
-        _refuse(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
@@ -683,7 +678,7 @@ def _cuda_device(t):
     """Number of the current device, which the call's tensors must be on."""
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
-    return torch.cuda.current_device()
+    return _current_device()
 
 
 def _stream_of(stream, device):
@@ -712,6 +707,38 @@ def _gdr_sizes(q, v, cu_seqlens):
     return 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1, T, HK, v.shape[1], D
 
 
+def _gdr_forward(q, k, v, g, beta, o, initial_state, final_state, cu_seqlens, one_token=False):
+    """Checks the tensors of a forward call and returns its addresses and sizes: (q, k, v, g, beta),
+    initial_state, cu_seqlens, (N, T, HK, HV, D, dtype), o, final_state, device."""
+    N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
+    if one_token:
+        N = T
+    dev, f32 = _cuda_device(q), torch.float32
+    dt, qk, vo, heads, sq = q.dtype, q.shape, (T, HV, D), (T, HV), (N, HV, D, D)
+    s0, sN, cu = initial_state, final_state, cu_seqlens
+    if not (k.shape == qk and v.shape == vo and o.shape == vo and g.shape == heads
+            and beta.shape == heads and k.dtype is dt and v.dtype is dt and g.dtype is f32
+            and beta.dtype is f32 and o.dtype is f32 and q.is_contiguous() and k.is_contiguous()
+            and v.is_contiguous() and g.is_contiguous() and beta.is_contiguous()
+            and o.is_contiguous() and q.get_device() == dev and k.get_device() == dev
+            and v.get_device() == dev and g.get_device() == dev and beta.get_device() == dev
+            and o.get_device() == dev
+            and (s0 is None or (s0.shape == sq and s0.dtype is f32 and s0.is_contiguous()
+                                and s0.get_device() == dev))
+            and (sN is None or sN is s0 or (sN.shape == sq and sN.dtype is f32 and sN.is_contiguous()
+                                            and sN.get_device() == dev))
+            and (cu is None or (cu.dim() == 1 and cu.dtype is torch.int32 and cu.is_contiguous()
+                                and cu.get_device() == dev))):
+        _gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev)
+        _p(cu, "cu_seqlens", (N + 1,), torch.int32, dev)
+        _p(o, "o", vo, f32, dev)
+        _p(s0, "initial_state", sq, f32, dev)
+        _p(sN, "final_state", sq, f32, dev)
+    return ((q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr()),
+            None if s0 is None else s0.data_ptr(), None if cu is None else cu.data_ptr(),
+            (N, T, HK, HV, D, _dtype(q)), o.data_ptr(), None if sN is None else sN.data_ptr(), dev)
+
+
 def _gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev):
     dt, qk, heads = q.dtype, (T, HK, D), (T, HV)
     return (_p(q, "q", qk, dt, dev), _p(k, "k", qk, dt, dev), _p(v, "v", (T, HV, D), dt, dev),
@@ -722,25 +749,16 @@ def kda_gdr_recurrent(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=
                       final_state=None, cu_seqlens=None, stream=None):
     """Gated delta rule with one decay per head, token by token: writes ``o`` [T, HV, D] and
     optionally ``final_state`` (which may be ``initial_state``)."""
-    N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
-    dev, f32, sq = _cuda_device(q), torch.float32, (N, HV, D, D)
-    _check(lib.kda_gdr_recurrent(
-        *_gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev), scale,
-        _p(initial_state, "initial_state", sq, f32, dev),
-        _p(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, HK, HV, D, _dtype(q),
-        _p(o, "o", (T, HV, D), f32, dev), _p(final_state, "final_state", sq, f32, dev),
-        _stream_of(stream, dev)))
+    x, s0, cu, sizes, op, sN, dev = _gdr_forward(q, k, v, g, beta, o, initial_state, final_state,
+                                                 cu_seqlens)
+    _check(lib.kda_gdr_recurrent(*x, scale, s0, cu, *sizes, op, sN, _stream_of(stream, dev)))
 
 
 def kda_gdr_decode_step(q, k, v, g, beta, state, o, *, scale: float = 1.0, stream=None):
     """One new token for each of N sequences (``q, k`` [N, HK, D], ``v, o`` [N, HV, D]);
     updates ``state`` [N, HV, D, D] in place."""
-    _, N, HK, HV, D = _gdr_sizes(q, v, None)
-    dev, f32 = _cuda_device(q), torch.float32
-    _check(lib.kda_gdr_decode_step(
-        *_gdr_inputs(q, k, v, g, beta, N, HK, HV, D, dev), scale,
-        _p(state, "state", (N, HV, D, D), f32, dev), N, HK, HV, D, _dtype(q),
-        _p(o, "o", (N, HV, D), f32, dev), _stream_of(stream, dev)))
+    x, s0, _, sizes, op, _, dev = _gdr_forward(q, k, v, g, beta, o, state, state, None, True)
+    _check(lib.kda_gdr_decode_step(*x, scale, s0, sizes[0], *sizes[2:], op, _stream_of(stream, dev)))
 
 
 def kda_gdr_chunk_fwd_workspace_bytes(N: int, T: int, HK: int, HV: int, D: int,
@@ -757,18 +775,14 @@ def kda_gdr_chunk_fwd(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=
     ``workspace``: ``"auto"`` takes the scratch from torch's caching allocator; a uint8 CUDA
     tensor of :func:`kda_gdr_chunk_fwd_workspace_bytes` is used as given; ``None`` runs
     :func:`kda_gdr_recurrent`.  fp32 inputs and D below 64 run the recurrent form."""
-    N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
-    dev, f32, sq, dt = _cuda_device(q), torch.float32, (N, HV, D, D), _dtype(q)
+    x, s0, cu, sizes, op, sN, dev = _gdr_forward(q, k, v, g, beta, o, initial_state, final_state,
+                                                 cu_seqlens)
     nbytes = 0
-    if workspace is not None and isinstance(workspace, str):
-        nbytes = lib.kda_gdr_chunk_fwd_workspace_bytes(N, T, HK, HV, D, dt)
+    if isinstance(workspace, str):
+        nbytes = lib.kda_gdr_chunk_fwd_workspace_bytes(*sizes)
     ws, nbytes, _keep = _scratch(workspace, nbytes, dev, q)
-    _check(lib.kda_gdr_chunk_fwd_ws(
-        *_gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev), scale,
-        _p(initial_state, "initial_state", sq, f32, dev),
-        _p(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, HK, HV, D, dt,
-        _p(o, "o", (T, HV, D), f32, dev), _p(final_state, "final_state", sq, f32, dev), ws, nbytes,
-        _stream_of(stream, dev)))
+    _check(lib.kda_gdr_chunk_fwd_ws(*x, scale, s0, cu, *sizes, op, sN, ws, nbytes,
+                                    _stream_of(stream, dev)))
 
 
 def kda_gdr_chunk_bwd_workspace_bytes(N: int, T: int, HK: int, HV: int, D: int,
@@ -821,19 +835,30 @@ def kda_prologue_bwd(x, conv_w, dq, dk, dv, dx, d_conv_w=None, *, H: int, D: int
     ``d_cache_in`` (x's dtype).  ``dq, dk, dv`` [T, H, D] share a dtype of their own."""
     T, C = x.shape[0], 3 * H * D
     N = 1 if cu_seqlens is None else cu_seqlens.shape[0] - 1
-    dev, f32, act, gt, thd = _cuda_device(x), torch.float32, x.dtype, dq.dtype, (T, H, D)
+    dev, f32, act, gt = _cuda_device(x), torch.float32, x.dtype, dq.dtype
+    tc, thd, wc = (T, C), (T, H, D), (C, 4)
+    if not (x.shape == tc and dx.shape == tc and conv_w.shape == wc and dq.shape == thd
+            and dk.shape == thd and dv.shape == thd and dx.dtype is act and conv_w.dtype is f32
+            and dk.dtype is gt and dv.dtype is gt and x.is_contiguous() and dx.is_contiguous()
+            and conv_w.is_contiguous() and dq.is_contiguous() and dk.is_contiguous()
+            and dv.is_contiguous() and x.get_device() == dev and dx.get_device() == dev
+            and conv_w.get_device() == dev and dq.get_device() == dev and dk.get_device() == dev
+            and dv.get_device() == dev):
+        for t, name, shape, kind in ((x, "x", tc, act), (conv_w, "conv_w", wc, f32),
+                                     (dq, "dq", thd, gt), (dk, "dk", thd, gt), (dv, "dv", thd, gt),
+                                     (dx, "dx", tc, act)):
+            _p(t, name, shape, kind, dev)
     dt = _dtype(x)
     nbytes = 0
     if d_conv_w is not None and isinstance(workspace, str):
         nbytes = lib.kda_prologue_bwd_workspace_bytes(N, T, H, D, dt)
     ws, nbytes, _keep = _scratch(workspace, nbytes, dev, x)
     _check(lib.kda_prologue_bwd(
-        _p(x, "x", (T, C), act, dev), _p(conv_w, "conv_w", (C, 4), f32, dev),
-        _p(cache_in, "cache_in", (N, 3, C), act, dev),
+        x.data_ptr(), conv_w.data_ptr(), _p(cache_in, "cache_in", (N, 3, C), act, dev),
         _p(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, H, D, dt, _dtype(dq),
-        _p(dq, "dq", thd, gt, dev), _p(dk, "dk", thd, gt, dev), _p(dv, "dv", thd, gt, dev),
-        _p(dx, "dx", (T, C), act, dev), _p(d_conv_w, "d_conv_w", (C, 4), f32, dev),
-        _p(d_cache_in, "d_cache_in", (N, 3, C), act, dev), ws, nbytes, _stream_of(stream, dev)))
+        dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dx.data_ptr(),
+        _p(d_conv_w, "d_conv_w", wc, f32, dev), _p(d_cache_in, "d_cache_in", (N, 3, C), act, dev), ws,
+        nbytes, _stream_of(stream, dev)))
 
 
 def kda_output_epilogue_bwd_workspace_bytes(T: int, H: int, D: int) -> int:
@@ -849,12 +874,22 @@ def kda_output_epilogue_bwd(o, gate, weight, d_out, d_o, d_gate, d_weight=None, 
         raise ValueError("o has three dimensions: tokens, heads, channels")
     thd = T, H, D = o.shape
     dev, f32, dt = _cuda_device(o), torch.float32, gate.dtype
+    if not (gate.shape == thd and d_out.shape == thd and d_o.shape == thd and d_gate.shape == thd
+            and weight.shape == (D,) and o.dtype is f32 and weight.dtype is f32 and d_o.dtype is f32
+            and d_out.dtype is dt and d_gate.dtype is dt and o.is_contiguous()
+            and gate.is_contiguous() and weight.is_contiguous() and d_out.is_contiguous()
+            and d_o.is_contiguous() and d_gate.is_contiguous() and o.get_device() == dev
+            and gate.get_device() == dev and weight.get_device() == dev
+            and d_out.get_device() == dev and d_o.get_device() == dev and d_gate.get_device() == dev):
+        for t, name, kind in ((o, "o", f32), (gate, "gate", dt), (d_out, "d_out", dt),
+                              (d_o, "d_o", f32), (d_gate, "d_gate", dt)):
+            _p(t, name, thd, kind, dev)
+        _p(weight, "weight", (D,), f32, dev)
     nbytes = 0
     if d_weight is not None and isinstance(workspace, str):
         nbytes = lib.kda_output_epilogue_bwd_workspace_bytes(T, H, D)
     ws, nbytes, _keep = _scratch(workspace, nbytes, dev, o)
     _check(lib.kda_output_epilogue_bwd(
-        _p(o, "o", thd, f32, dev), _p(gate, "gate", thd, dt, dev),
-        _p(weight, "weight", (D,), f32, dev), eps, _p(d_out, "d_out", thd, dt, dev), T, H, D,
-        _dtype(gate), _p(d_o, "d_o", thd, f32, dev), _p(d_gate, "d_gate", thd, dt, dev),
-        _p(d_weight, "d_weight", (D,), f32, dev), ws, nbytes, _stream_of(stream, dev)))
+        o.data_ptr(), gate.data_ptr(), weight.data_ptr(), eps, d_out.data_ptr(), T, H, D,
+        _dtype(gate), d_o.data_ptr(), d_gate.data_ptr(), _p(d_weight, "d_weight", (D,), f32, dev), ws,
+        nbytes, _stream_of(stream, dev)))

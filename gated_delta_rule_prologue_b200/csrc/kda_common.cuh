@@ -204,6 +204,18 @@ __device__ __forceinline__ float bounded_gate(float graw, float a, float bias, f
 }
 
 // ---------------------------------------------------------------------------
+// Kernels launched behind one another in one call (launch_behind below): the second one's CTAs may
+// be set up while the first one ends, and wait here for all its writes.
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ void wait_for_previous_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void next_kernel_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Device status word (one per device, a file-scope device variable)
 // ---------------------------------------------------------------------------
 
@@ -274,6 +286,23 @@ __device__ __forceinline__ int seq_of_token(const int32_t *cu, int N, int t) {
 
 // Host-side launchers implemented in the kernel files, called by kda_api.cu.
 namespace kda {
+// Launches a kernel that starts with wait_for_previous_kernel(): its launch overlaps the end of the
+// kernel before it in the stream (about 2 us less between the two on an idle GPU).
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                          A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
 // Device addresses of the file-scope __device__ status word (kda_status.cu)
 // and of the fixed scratch of kda_chunk_fwd_static (kda_static.cu) on the
 // current device, looked up once per device.

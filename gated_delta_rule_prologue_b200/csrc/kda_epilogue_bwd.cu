@@ -101,6 +101,7 @@ epilogue_bwd_kernel(const float *__restrict__ o, const Tg *__restrict__ gate,
       }
     }
   }
+  next_kernel_may_start();
   if (partial == nullptr) return;
   // The warp's rows share channels: lanes LPR apart; then the warps, in order.
 #pragma unroll
@@ -124,6 +125,7 @@ epilogue_bwd_kernel(const float *__restrict__ o, const Tg *__restrict__ gate,
 template <int D>
 __global__ void __launch_bounds__(256)
 epilogue_bwd_weight_kernel(const float *__restrict__ partial, int n, float *__restrict__ d_weight) {
+  wait_for_previous_kernel();
   __shared__ double part[32][8];
   const int c = threadIdx.x & 7, slice = threadIdx.x >> 3;
   const float *p = partial + 8 * blockIdx.x + c;
@@ -157,9 +159,10 @@ cudaError_t launch_typed(const float *o, const void *gate, const float *weight, 
     epilogue_bwd_kernel<Tg, D><<<ctas, kThreads, 0, s>>>(
         o, static_cast<const Tg *>(gate), weight, eps, static_cast<const Tg *>(d_out), rows, d_o,
         static_cast<Tg *>(d_gate), partial);
-  if (d_weight != nullptr && ctas != 1)
-    epilogue_bwd_weight_kernel<D><<<D / 8, 256, 0, s>>>(ws, ctas, d_weight);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || d_weight == nullptr || ctas == 1) return e;
+  return launch_behind(epilogue_bwd_weight_kernel<D>, dim3(D / 8), 256, 0, s, (const float *)ws, ctas,
+                       d_weight);
 }
 
 template <typename Tg>

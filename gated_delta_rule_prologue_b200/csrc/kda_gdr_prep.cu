@@ -362,6 +362,7 @@ gdr_prep_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const floa
           sum[i][e][f] = fmaf(f >> 1 ? t1s.s : t0s.s, y[e][f] + y2[e][f], sum[i][e][f]);
     }
   }
+  next_kernel_may_start();
   // Scales of T's rows (its columns are spread over the warps).
 #pragma unroll
   for (int i = 0; i < 4; ++i) {

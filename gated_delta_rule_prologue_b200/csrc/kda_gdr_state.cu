@@ -84,6 +84,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
            v + ((size_t)(t0 + min(r, len - 1)) * HV + h) * D + part * NW * 16 + p * 8, r < len);
     }
   };
+  wait_for_previous_kernel();
   if (chunks > 0) load(0);
   cp_commit();
 
@@ -281,6 +282,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
     __syncthreads();  // the other buffer is free for the chunk after next
   }
   cp_wait<0>();
+  next_kernel_may_start();
 
   if (sN) {
     float *p = sN + ((size_t)nh * D + row) * D + col;
@@ -301,10 +303,9 @@ cudaError_t launch_nw(const void *v, const float *s0, const int32_t *cu, float s
   if (e != cudaSuccess) return e;
   const long long ctas = (long long)N * HV * (D / (16 * NW));
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
-  kern<<<(unsigned)ctas, NW * 32, bytes, s>>>(static_cast<const Tin *>(v), s0, cu, scale, N, T, HK,
-                                              HV, static_cast<uint8_t *>(ws),
-                                              layout(N, T, HK, HV, D, kKeep), o, sN, status);
-  return cudaGetLastError();
+  return launch_behind(kern, dim3((unsigned)ctas), NW * 32, bytes, s, static_cast<const Tin *>(v), s0,
+                       cu, scale, N, T, HK, HV, static_cast<uint8_t *>(ws),
+                       layout(N, T, HK, HV, D, kKeep), o, sN, status);
 }
 
 template <typename Tin, bool kKeep>

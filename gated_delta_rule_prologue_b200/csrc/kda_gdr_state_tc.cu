@@ -383,6 +383,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       }
     };
     if (warp == kChainWarps) {
+      wait_for_previous_kernel();
       load(0);
       if (chunks > 1) load(1);
     }
@@ -510,10 +511,8 @@ cudaError_t launch_typed(const void *v, const float *s0, const int32_t *cu, floa
   const long long ctas = (long long)N * HV;
   CUtensorMap tm;
   if (ctas >= (1LL << 31) || !make_v_map(&tm, v, dt, HV, T)) return cudaErrorInvalidValue;
-  kern<<<(unsigned)ctas, kThreads, kSmem, s>>>(tm, s0, cu, scale, N, T, HK, HV,
-                                               static_cast<uint8_t *>(ws),
-                                               layout(N, T, HK, HV, D, kKeep), o, sN, status);
-  return cudaGetLastError();
+  return launch_behind(kern, dim3((unsigned)ctas), kThreads, kSmem, s, tm, s0, cu, scale, N, T, HK, HV,
+                       static_cast<uint8_t *>(ws), layout(N, T, HK, HV, D, kKeep), o, sN, status);
 }
 
 }  // namespace

@@ -254,6 +254,7 @@ prologue_bwd_kernel(const Tin *__restrict__ x, const float *__restrict__ w,
     }
     ta = tb;
   }
+  next_kernel_may_start();
   if (partial != nullptr && active) {
     float4 *to = reinterpret_cast<float4 *>(partial) + (size_t)blockIdx.y * Cn + c0;
 #pragma unroll
@@ -269,6 +270,7 @@ prologue_bwd_kernel(const Tin *__restrict__ x, const float *__restrict__ w,
 __global__ void __launch_bounds__(256)
 prologue_bwd_weight_kernel(const float4 *__restrict__ partial, int tiles, int Cn,
                            float4 *__restrict__ dw) {
+  wait_for_previous_kernel();
   __shared__ double4 part[8][32];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
   double4 t = {0.0, 0.0, 0.0, 0.0};
@@ -290,23 +292,22 @@ prologue_bwd_weight_kernel(const float4 *__restrict__ partial, int tiles, int Cn
 
 int channel_blocks(int Cn) { return (Cn / 4 + kThreads - 1) / kThreads; }
 
-// Tokens per tile: the CTAs run in waves of two per SM, and a tile costs its tokens plus about 16
-// more (three halo tokens, filling the pipeline, a row of dw written and read).  The length with
-// the least waves x cost: 8192 tokens x 96 heads of 128 in one wave of 344 tokens take 150 us where
-// 64-token tiles (5.2 waves) took 182.
+// Tokens per tile: as many tiles as fill two CTAs per SM once, a multiple of four tokens each, up
+// to 512 (then more waves).  A tile costs about 16 tokens beside its own (three halo tokens, filling
+// the pipeline, a row of dw written and read), so one wave of long tiles beats several of short
+// ones: 8192 tokens x 96 heads of 128 in 344-token tiles take 168 us, in 64-token tiles (5.2 waves)
+// 182.
 int tile_of(int T, int Cn) {
   const long long blocks = channel_blocks(Cn), slots = 2 * 148;
-  long long best = 1LL << 60;
-  int tile = 4;
-  for (int t = 4; t <= 512; t += 4) {
-    const long long tiles = (T + t - 1) / t, cost = (blocks * tiles + slots - 1) / slots * (t + 16);
-    if (tiles <= 65535 && cost < best) {  // the grid's second dimension
-      best = cost;
-      tile = t;
-    }
+  const long long wave = blocks < slots ? slots / blocks : 1;
+  long long tile = (T + wave - 1) / wave;
+  if (tile > 512) {
+    const long long waves = (tile + 511) / 512;
+    tile = (T + wave * waves - 1) / (wave * waves);
   }
-  while ((T + (long long)tile - 1) / tile > 65535) tile *= 2;
-  return tile;
+  tile = tile < 4 ? 4 : (tile + 3) / 4 * 4;
+  while ((T + tile - 1) / tile > 65535) tile *= 2;  // the grid's second dimension
+  return (int)tile;
 }
 
 template <typename Tin, typename Tg, int D>
@@ -321,9 +322,11 @@ cudaError_t launch_typed(const void *x, const float *w, const void *cache_in, co
       static_cast<const Tin *>(x), w, static_cast<const Tin *>(cache_in), cu, N, T, H,
       static_cast<const Tg *>(dq), static_cast<const Tg *>(dk), static_cast<const Tg *>(dv), tile,
       static_cast<Tin *>(dx), static_cast<Tin *>(d_cache), partial, status);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   if (dw != nullptr && tiles > 1)
-    prologue_bwd_weight_kernel<<<(Cn + 31) / 32, 256, 0, s>>>(
-        static_cast<const float4 *>(ws), tiles, Cn, reinterpret_cast<float4 *>(dw));
+    return launch_behind(prologue_bwd_weight_kernel, dim3((Cn + 31) / 32), 256, 0, s,
+                         static_cast<const float4 *>(ws), tiles, Cn, reinterpret_cast<float4 *>(dw));
   return cudaGetLastError();
 }
 
