@@ -53,14 +53,49 @@ __host__ __device__ constexpr uint32_t kq_bytes(int D) { return kq_tile_bytes(D)
 __host__ __device__ inline long long slots(int N, int T) { return (long long)T / C + N + 1; }
 __host__ __device__ inline long long first_slot(int bos, int n) { return bos / C + n; }
 
+// Segments of the forward's state pass.  The chunks' effect on the state is affine, S -> M S + B, and
+// with few (sequence, head) pairs most SMs would wait for a long sequence's chain of chunks.  Then
+// sequences are cut into segments of L chunks: a map pass finds every segment's B (from a zero or the
+// initial state) and M (its effect on the identity), a scan composes the segments' first states,
+// and the read-out pass runs all segments at once.  Segment g of sequence n has slot
+// bos / (64 L) + n + g, as chunks have theirs.
+__host__ __device__ inline long long segment_slots(int N, int T, int L) {
+  return (long long)T / ((long long)C * L) + N + 1;
+}
+// Chunks per segment (0: whole sequences), by a model of B200 measurements for sequences of about
+// T / N tokens: a chunk takes 4.9 us with the read-out and 4.1 without, one CTA of 64 value channels
+// runs per SM, a step of the scan takes 6 us, and the two more launches with their first loads 10.
+// Cutting has to save a tenth.  One prompt of 4096 tokens and 8 heads: 337 -> 166 us.
+inline int segment_chunks(int N, int T, int HV, int D) {
+  const long long ctas = (long long)N * HV * (D / 64);
+  if (N < 1 || T < 1 || ctas > 148) return 0;
+  const long long n = (((long long)T + N - 1) / N + C - 1) / C;
+  double best = 0.9 * 4.9 * (double)n;
+  int len = 0;
+  for (long long G = 2; G <= n / 2 && G <= 64; ++G) {
+    const long long L = (n + G - 1) / G, Gs = (n + L - 1) / L;
+    if (Gs < 2) continue;
+    const long long maps = ctas * (2 * Gs - 3), reads = ctas * Gs;
+    const double t = (double)((maps + 147) / 148) * L * 4.1 + (double)((reads + 147) / 148) * L * 4.9 +
+                     6.0 * (double)(Gs - 2) + 10.0;
+    if (t < best) {
+      best = t;
+      len = (int)L;
+    }
+  }
+  return len;
+}
+
 // Byte offsets in the workspace.
 struct Layout {
   size_t kq, tp;                 // records
   size_t state, dstate, u, x;    // backward: per chunk fp32 S and dS' (key-major: [key][value channel]),
                                  // U and X [64][D]
+  int seg_chunks;                // forward: chunks per segment, or 0
+  size_t seg_m, seg_b, seg_e;    // and per segment fp32 M, B and first state, each stored like a state
   size_t bytes;
 };
-__host__ __device__ inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
+inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
   const size_t n = (size_t)slots(N, T);
   Layout l;
   l.kq = 0;
@@ -70,7 +105,13 @@ __host__ __device__ inline Layout layout(int N, int T, int HK, int HV, int D, bo
   l.dstate = l.state + (bwd ? sq : 0);
   l.u = l.dstate + (bwd ? sq : 0);
   l.x = l.u + (bwd ? rows : 0);
-  l.bytes = l.x + (bwd ? rows : 0);
+  l.seg_m = l.x + (bwd ? rows : 0);
+  l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV, D);
+  const size_t seg =
+      l.seg_chunks ? (size_t)segment_slots(N, T, l.seg_chunks) * HV * (size_t)D * D * 4 : 0;
+  l.seg_b = l.seg_m + seg;
+  l.seg_e = l.seg_b + seg;
+  l.bytes = l.seg_e + seg;
   return l;
 }
 
@@ -105,15 +146,15 @@ __device__ __forceinline__ float load_g(const float *g0, size_t stride, int t, i
   return t < len ? floor_g(__ldg(g0 + t * stride)) : 0.f;
 }
 
-// Sequence and chunk of a slot; false for a slot that no chunk has.
-__device__ __forceinline__ bool chunk_of_slot(const int32_t *cu, int N, int T, long long slot,
-                                              int *status, int &n, int &bos, int &eos, int &c) {
+// Sequence of a slot and the slot's place in it, for slots of `span` tokens (a chunk, or a segment).
+__device__ __forceinline__ long long place_of_slot(const int32_t *cu, int N, int T, long long slot,
+                                                   int span, int *status, int &n, int &bos, int &eos) {
   int lo = 0, hi = N - 1;
   n = 0;
   if (cu) {
     while (lo <= hi) {
       const int mid = (lo + hi) >> 1;
-      if (first_slot(cu[mid], mid) <= slot) {
+      if (cu[mid] / span + mid <= slot) {
         n = mid;
         lo = mid + 1;
       } else {
@@ -122,7 +163,12 @@ __device__ __forceinline__ bool chunk_of_slot(const int32_t *cu, int N, int T, l
     }
   }
   seq_bounds(cu, n, T, status, bos, eos);
-  const long long cc = slot - first_slot(bos, n);
+  return slot - (bos / span + n);
+}
+// Sequence and chunk of a slot; false for a slot that no chunk has.
+__device__ __forceinline__ bool chunk_of_slot(const int32_t *cu, int N, int T, long long slot,
+                                              int *status, int &n, int &bos, int &eos, int &c) {
+  const long long cc = place_of_slot(cu, N, T, slot, C, status, n, bos, eos);
   if (cc < 0 || cc * C >= eos - bos) return false;
   c = (int)cc;
   return true;
@@ -265,6 +311,56 @@ __device__ __forceinline__ void split_a(const float (&c)[NT][4], int kk, const S
 template <int NT> __device__ __forceinline__ void zero(float (&c)[NT][4]) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.f;
+}
+
+// A matrix of fp32 rows of D values becomes, in its place, one of split rows: per row D fp16 hi,
+// then D fp16 lo (4 D bytes as before), the 16-byte pieces of each XOR-swizzled by the row, so that
+// ldmatrix reads eight rows without bank conflicts.  A warp owns whole rows: no block barrier.
+template <int D> __device__ __forceinline__ uint32_t row_off(int row, int c8) {
+  return (uint32_t)(row * 4 * D + ((c8 ^ (row & 7)) << 4));
+}
+// B operand whose columns (n) are rows n0 .. n0 + 15; lo: the second term.
+template <int D>
+__device__ __forceinline__ void load_rows_b(uint32_t (&r)[4], uint32_t base, int n0, int k0, bool lo) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4(r, base + row_off<D>(n0 + (m >> 1) * 8 + (lane & 7), (k0 >> 3) + (m & 1)) + (lo ? 2 * D : 0));
+}
+// A operand of rows m0 .. m0 + 15.
+template <int D>
+__device__ __forceinline__ void load_rows_a(uint32_t (&r)[4], uint32_t base, int m0, int k0, bool lo) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4(r, base + row_off<D>(m0 + (m & 1) * 8 + (lane & 7), (k0 >> 3) + (m >> 1)) + (lo ? 2 * D : 0));
+}
+
+// B operand whose k are rows k0 .. k0 + 15.
+template <int D>
+__device__ __forceinline__ void load_rows_bt(uint32_t (&r)[4], uint32_t base, int n0, int k0, bool lo) {
+  const int lane = threadIdx.x & 31, m = lane >> 3;
+  ldsm4t(r, base + row_off<D>(k0 + (m & 1) * 8 + (lane & 7), (n0 >> 3) + (m >> 1)) + (lo ? 2 * D : 0));
+}
+// A warp splits its `rows` rows from row0 on (a multiple of four accesses of 128 / D rows).
+template <int D>
+__device__ __forceinline__ void split_rows_in_place(uint8_t *base, int row0, int rows, float inv) {
+  constexpr int LR = D / 4, RP = 32 / LR;  // lanes per row, rows per warp access
+  const int lane = threadIdx.x & 31, rl = lane / LR, cl = lane % LR;
+#pragma unroll 1
+  for (int i = 0; i < rows; i += 4 * RP) {
+    float4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x[k] = *reinterpret_cast<const float4 *>(base + (row0 + i + k * RP + rl) * 4 * D + 16 * cl);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint2 hi, lo;
+      split2(x[k].x, x[k].y, inv, hi.x, lo.x);
+      split2(x[k].z, x[k].w, inv, hi.y, lo.y);
+      const uint32_t o = row_off<D>(row0 + i + k * RP + rl, cl >> 1) + 8 * (cl & 1);
+      *reinterpret_cast<uint2 *>(base + o) = hi;
+      *reinterpret_cast<uint2 *>(base + o + 2 * D) = lo;
+    }
+    __syncwarp();
+  }
 }
 
 }  // namespace gdr

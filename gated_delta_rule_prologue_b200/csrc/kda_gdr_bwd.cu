@@ -275,25 +275,6 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
 
 constexpr int kLocalThreads = 256;
 
-// A matrix of fp32 rows of D values becomes, in its place, one of split rows: per row D fp16 hi,
-// then D fp16 lo (4 D bytes as before), the 16-byte pieces of each XOR-swizzled by the row, so that
-// ldmatrix reads eight rows without bank conflicts.  A warp owns whole rows: no block barrier.
-template <int D> __device__ __forceinline__ uint32_t row_off(int row, int c8) {
-  return (uint32_t)(row * 4 * D + ((c8 ^ (row & 7)) << 4));
-}
-// B operand whose columns (n) are rows n0 .. n0 + 15; lo: the second term.
-template <int D>
-__device__ __forceinline__ void load_rows_b(uint32_t (&r)[4], uint32_t base, int n0, int k0, bool lo) {
-  const int lane = threadIdx.x & 31, m = lane >> 3;
-  ldsm4(r, base + row_off<D>(n0 + (m >> 1) * 8 + (lane & 7), (k0 >> 3) + (m & 1)) + (lo ? 2 * D : 0));
-}
-// A operand of rows m0 .. m0 + 15.
-template <int D>
-__device__ __forceinline__ void load_rows_a(uint32_t (&r)[4], uint32_t base, int m0, int k0, bool lo) {
-  const int lane = threadIdx.x & 31, m = lane >> 3;
-  ldsm4(r, base + row_off<D>(m0 + (m & 1) * 8 + (lane & 7), (k0 >> 3) + (m >> 1)) + (lo ? 2 * D : 0));
-}
-
 template <int D> struct LocalSmem {
   static constexpr uint32_t kK = 0, kQ = kQRows;
   static constexpr uint32_t kS = kq_tile_bytes(D);   // S, D rows (key channels)
@@ -397,27 +378,6 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
     tc::mbar_arrive_expect_tx(&sm.states, 2 * D * D * 4);
     tc::bulk_load(smem + Sm::kS, ws + lay.state + rec * D * D * 4, D * D * 4, &sm.states);
     tc::bulk_load(smem + Sm::kD, ws + lay.dstate + rec * D * D * 4, D * D * 4, &sm.states);
-  };
-  // Rows of a warp in place: `rows` rows from row0 on, in batches of four accesses.
-  auto split_rows = [&](uint32_t base, int row0, int rows, float inv) {
-#pragma unroll 1
-    for (int i = 0; i < rows; i += 4 * RP) {
-      float4 x[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        x[k] = *reinterpret_cast<const float4 *>(smem + base + (row0 + i + k * RP + rl) * 4 * D + 16 * cl);
-      __syncwarp();
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint2 hi, lo;
-        split2(x[k].x, x[k].y, inv, hi.x, lo.x);
-        split2(x[k].z, x[k].w, inv, hi.y, lo.y);
-        const uint32_t o = base + row_off<D>(row0 + i + k * RP + rl, cl >> 1) + 8 * (cl & 1);
-        *reinterpret_cast<uint2 *>(smem + o) = hi;
-        *reinterpret_cast<uint2 *>(smem + o + 2 * D) = lo;
-      }
-      __syncwarp();
-    }
   };
   // A warp's 8 of 64 rows, held in registers, with a scale per row.
   constexpr int kHeld = 8 / RP;
@@ -523,8 +483,8 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
       }
       big = block_max2(big.x, big.y, sm.red);
       const Scale ss = scale_of(big.x), ds = scale_of(big.y);
-      split_rows(Sm::kS, kRows * warp, kRows, ss.inv);
-      split_rows(Sm::kD, kRows * warp, kRows, ds.inv);
+      split_rows_in_place<D>(smem + Sm::kS, kRows * warp, kRows, ss.inv);
+      split_rows_in_place<D>(smem + Sm::kD, kRows * warp, kRows, ds.inv);
       cp_wait<0>();  // this thread's part of its own warp's rows of dO
       __syncwarp();
       split_own(Sm::kA, sm.as);

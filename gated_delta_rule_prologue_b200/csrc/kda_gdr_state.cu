@@ -47,9 +47,14 @@ __device__ __forceinline__ float2 widen2(uint32_t u, __half) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
-// kKeep: the backward's forward: S at the start of every chunk and U go to the workspace, and
-// there is no read-out.
-template <typename Tin, int D, int NW, bool kKeep>
+// What a launch of the pass is for.
+enum Role {
+  kOut,   // the read-out and the last states; of segments from the scan's states, if sequences are cut
+  kKeep,  // the backward's forward: S at the start of every chunk and U go to the workspace
+  kMap    // a segment's B (kind 0) or M (kind 1); not of a sequence's last segment, nor M of its first
+};
+
+template <typename Tin, int D, int NW, int kRole>
 __global__ void __launch_bounds__(NW * 32, 1)
 gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__restrict__ cu,
                  float scale, int N, int T, int HK, int HV, uint8_t *__restrict__ ws, Layout lay,
@@ -58,15 +63,35 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   constexpr int NT = D / 8, KK = D / 16;
   constexpr int kParts = D / (16 * NW);  // CTAs per head
   extern __shared__ __align__(128) uint8_t smem[];
+  wait_for_previous_kernel();  // before any way out: what comes next takes this one's end for the last one's
   const uint32_t sbase = smem_addr(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = blockIdx.x % kParts, nh = blockIdx.x / kParts;
-  const int n = nh / HV, h = nh % HV, hk = h / (HV / HK);
-  int bos, eos;
-  seq_bounds(cu, n, T, status, bos, eos);
-  const int chunks = (eos - bos + C - 1) / C;
+  int b = blockIdx.x;
+  const int part = b % kParts;
+  b /= kParts;
+  const int kind = kRole == kMap ? b & 1 : 0;
+  if (kRole == kMap) b >>= 1;
+  const int h = b % HV, hk = h / (HV / HK);
+  int n = b / HV, bos, eos, first = 0, end;   // chunks first .. end - 1 of sequence n
+  const int L = kRole == kKeep ? 0 : lay.seg_chunks;
+  size_t seg = 0;                             // the segment's (slot, head)
+  if (L == 0) {
+    seq_bounds(cu, n, T, status, bos, eos);
+    end = (eos - bos + C - 1) / C;
+  } else {
+    const long long slot = n;
+    const long long g = place_of_slot(cu, N, T, slot, C * L, status, n, bos, eos);
+    end = (eos - bos + C - 1) / C;
+    if (g < 0 || (g > 0 && g * L >= end) || !in_range(status, slot, segment_slots(N, T, L))) return;
+    first = (int)g * L;
+    if (kRole == kMap && (first + L >= end || (kind == 1 && g == 0))) return;
+    end = min(end, first + L);
+    seg = (size_t)slot * HV + h;
+  }
+  const bool is_last = end * C >= eos - bos;
   const long long slot0 = first_slot(bos, n);
-  if (!in_range(status, slot0 + chunks, slots(N, T) + 1)) return;
+  if (!in_range(status, slot0 + end, slots(N, T) + 1)) return;
+  const size_t nh = (size_t)n * HV + h;
   const int ch0 = (part * NW + warp) * 16;     // the warp's first value channel
   const int row = ch0 + lane / 4;              // and this lane's rows: row, row + 8
   const int col = 2 * (lane & 3);
@@ -84,14 +109,21 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
            v + ((size_t)(t0 + min(r, len - 1)) * HV + h) * D + part * NW * 16 + p * 8, r < len);
     }
   };
-  wait_for_previous_kernel();
-  if (chunks > 0) load(0);
+  if (first < end) load(first);
   cp_commit();
 
   float s[NT][4];
   zero(s);
-  if (s0) {
-    const float *p = s0 + ((size_t)nh * D + row) * D + col;
+  const float *from = first == 0 ? (s0 ? s0 + nh * D * D : nullptr)
+                      : kRole == kOut ? reinterpret_cast<const float *>(ws + lay.seg_e) + seg * D * D
+                                      : nullptr;
+  if (kRole == kMap && kind == 1) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = row + 8 * (e >> 1) == 8 * i + col + (e & 1) ? 1.f : 0.f;
+  } else if (from) {
+    const float *p = from + (size_t)row * D + col;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const float2 a = *reinterpret_cast<const float2 *>(p + 8 * i);
@@ -100,8 +132,8 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
     }
   }
 
-  for (int c = 0; c < chunks; ++c) {
-    if (c + 1 < chunks) load(c + 1);
+  for (int c = first; c < end; ++c) {
+    if (c + 1 < end) load(c + 1);
     cp_commit();
     cp_wait<1>();
     __syncthreads();
@@ -111,7 +143,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
     const float *vec = reinterpret_cast<const float *>(stp + Sm::kTp + kVec);
     const int t0 = bos + c * C, len = min(C, eos - t0);
 
-    if constexpr (kKeep) {
+    if constexpr (kRole == kKeep) {
       float *p = reinterpret_cast<float *>(ws + lay.state) + ((size_t)(slot0 + c) * HV + h) * D * D + row;
 #pragma unroll
       for (int i = 0; i < NT; ++i)
@@ -137,7 +169,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
         mma(ks[2 * np + 1], hi, b[2], b[3]);
         mma(ks[2 * np], lo, b[0], b[1]);
         mma(ks[2 * np + 1], lo, b[2], b[3]);
-        if constexpr (!kKeep) {
+        if constexpr (kRole == kOut) {
           load_b<kKq>(b, st + Sm::kQ, 16 * np, 16 * kk);
           mma(qs[2 * np], hi, b[0], b[1]);
           mma(qs[2 * np + 1], hi, b[2], b[3]);
@@ -159,7 +191,8 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
           const int i = 2 * np + e;
           const float2 g = *reinterpret_cast<const float2 *>(vec + kVecG * C + 8 * i + col);
           const float2 bt = *reinterpret_cast<const float2 *>(vec + kVecBeta * C + 8 * i + col);
-          const float2 v0 = widen2(b[2 * e], Tin{}), v1 = widen2(b[2 * e + 1], Tin{});
+          float2 v0 = widen2(b[2 * e], Tin{}), v1 = widen2(b[2 * e + 1], Tin{});
+          if (kRole == kMap && kind == 1) v0 = v1 = make_float2(0.f, 0.f);
           ks[i][0] = bt.x * (v0.x - g.x * (f0 * ks[i][0]));
           ks[i][1] = bt.y * (v0.y - g.y * (f0 * ks[i][1]));
           ks[i][2] = bt.x * (v1.x - g.x * (f1 * ks[i][2]));
@@ -197,13 +230,14 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
       u[i][2] *= r1.s * t.x;
       u[i][3] *= r1.s * t.y;
     }
-    if constexpr (kKeep) {
+    if constexpr (kRole == kKeep) {
       float *p = reinterpret_cast<float *>(ws + lay.u) + ((size_t)(slot0 + c) * HV + h) * C * D + row;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[(8 * i + col + (e & 1)) * D + 8 * (e >> 1)] = u[i][e];
-    } else {
+    }
+    if constexpr (kRole == kOut) {
       // O^T = scale (G (Q S)^T + U^T P^T).
       float pu[8][4];
       zero(pu);
@@ -284,8 +318,11 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   cp_wait<0>();
   next_kernel_may_start();
 
-  if (sN) {
-    float *p = sN + ((size_t)nh * D + row) * D + col;
+  float *to = is_last && sN ? sN + nh * D * D : nullptr;
+  if (kRole == kMap)
+    to = reinterpret_cast<float *>(ws + (kind ? lay.seg_m : lay.seg_b)) + seg * D * D;
+  if (to) {
+    float *p = to + (size_t)row * D + col;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
@@ -294,35 +331,154 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   }
 }
 
-template <typename Tin, int D, int NW, bool kKeep>
-cudaError_t launch_nw(const void *v, const float *s0, const int32_t *cu, float scale, int N, int T,
-                      int HK, int HV, void *ws, float *o, float *sN, int *status, cudaStream_t s) {
-  auto kern = gdr_state_kernel<Tin, D, NW, kKeep>;
+// First states of the segments: E_1 = B_0 and E_g+1 = M_g E_g + B_g, one CTA per (sequence, head).
+// E^T is the A operand of its own next step, as S^T in the pass above: a warp owns 16 value channels.
+// M (rows: its columns) is split in its place with one power of two, two matrices in shared memory.
+template <int D>
+__global__ void __launch_bounds__(2 * D, 1)
+gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *__restrict__ ws,
+                Layout lay, int *status) {
+  constexpr int NT = D / 8, KK = D / 16, kWarps = D / 16, kThreads = 2 * D;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float largest[kWarps];
+  wait_for_previous_kernel();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = blockIdx.x / HV, h = blockIdx.x % HV, L = lay.seg_chunks;
+  int bos, eos;
+  seq_bounds(cu, n, T, status, bos, eos);
+  const int G = ((eos - bos + C - 1) / C + L - 1) / L;
+  const long long slot0 = bos / (C * L) + n;
+  if (G < 2 || !in_range(status, slot0 + G, segment_slots(N, T, L) + 1)) return;
+  const int row = 16 * warp + lane / 4, col = 2 * (lane & 3);
+  auto block_of = [&](size_t area, int g) {
+    return reinterpret_cast<float *>(ws + area) + ((size_t)(slot0 + g) * HV + h) * D * D;
+  };
+  auto fetch = [&](int g) {
+    cp_block(smem_addr(smem) + (g & 1) * D * D * 4, reinterpret_cast<const uint8_t *>(block_of(lay.seg_m, g)),
+             D * D * 4);
+  };
+  if (G > 2) fetch(1);
+  cp_commit();
+  float s[NT][4];
+  {
+    const float *p = block_of(lay.seg_b, 0) + (size_t)row * D + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float2 a = *reinterpret_cast<const float2 *>(p + 8 * i);
+      const float2 b = *reinterpret_cast<const float2 *>(p + 8 * D + 8 * i);
+      s[i][0] = a.x; s[i][1] = a.y; s[i][2] = b.x; s[i][3] = b.y;
+    }
+  }
+  for (int g = 1;; ++g) {
+    float *p = block_of(lay.seg_e, g) + (size_t)row * D + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
+      *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
+    }
+    if (g + 1 >= G) break;
+    if (g + 2 < G) fetch(g + 1);
+    cp_commit();
+    cp_wait<1>();
+    __syncthreads();
+    uint8_t *mat = smem + (g & 1) * D * D * 4;
+    float big = 0.f;
+    for (int i = threadIdx.x; i < D * D / 4; i += kThreads) {
+      const float4 x = reinterpret_cast<const float4 *>(mat)[i];
+      big = fmaxf(fmaxf(fmaxf(big, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
+    if (lane == 0) largest[warp] = big;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) big = fmaxf(big, largest[i]);
+    const Scale ms = scale_of(big);
+    split_rows_in_place<D>(mat, 16 * warp, 16, ms.inv);
+    Scale a0, a1;
+    row_scales(s, a0, a1);
+    uint32_t hi[KK][4], lo[KK][4];
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) split_a(s, kk, a0, a1, hi[kk], lo[kk]);
+    __syncthreads();
+    const float f0 = ms.s * a0.s, f1 = ms.s * a1.s;
+    const float *bp = block_of(lay.seg_b, g) + (size_t)row * D + col;
+#pragma unroll
+    for (int j = 0; j < NT / 4; ++j) {
+      float acc[4][4];
+      zero(acc);
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+        for (int np = 0; np < 2; ++np) {
+          uint32_t b[4], bl[4];
+          load_rows_bt<D>(b, smem_addr(mat), 32 * j + 16 * np, 16 * kk, false);
+          load_rows_bt<D>(bl, smem_addr(mat), 32 * j + 16 * np, 16 * kk, true);
+          mma(acc[2 * np], hi[kk], b[0], b[1]);
+          mma(acc[2 * np + 1], hi[kk], b[2], b[3]);
+          mma(acc[2 * np], lo[kk], b[0], b[1]);
+          mma(acc[2 * np + 1], lo[kk], b[2], b[3]);
+          mma(acc[2 * np], hi[kk], bl[0], bl[1]);
+          mma(acc[2 * np + 1], hi[kk], bl[2], bl[3]);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = *reinterpret_cast<const float2 *>(bp + 32 * j + 8 * i);
+        const float2 y = *reinterpret_cast<const float2 *>(bp + 8 * D + 32 * j + 8 * i);
+        float(&t)[4] = s[4 * j + i];
+        t[0] = fmaf(f0, acc[i][0], x.x);
+        t[1] = fmaf(f0, acc[i][1], x.y);
+        t[2] = fmaf(f1, acc[i][2], y.x);
+        t[3] = fmaf(f1, acc[i][3], y.y);
+      }
+    }
+    __syncthreads();  // the matrix has been read: the next fetch may take its place
+  }
+  cp_wait<0>();
+}
+
+template <typename Tin, int D, int NW, int kRole>
+cudaError_t launch_role(const void *v, const float *s0, const int32_t *cu, float scale, int N, int T,
+                        int HK, int HV, void *ws, const Layout &lay, float *o, float *sN, int *status,
+                        cudaStream_t s) {
+  auto kern = gdr_state_kernel<Tin, D, NW, kRole>;
   const int bytes = (int)StateSmem<D, NW>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const long long ctas = (long long)N * HV * (D / (16 * NW));
+  const long long units = kRole != kKeep && lay.seg_chunks ? segment_slots(N, T, lay.seg_chunks) : N;
+  const long long ctas = units * HV * (D / (16 * NW)) * (kRole == kMap ? 2 : 1);
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
   return launch_behind(kern, dim3((unsigned)ctas), NW * 32, bytes, s, static_cast<const Tin *>(v), s0,
-                       cu, scale, N, T, HK, HV, static_cast<uint8_t *>(ws),
-                       layout(N, T, HK, HV, D, kKeep), o, sN, status);
+                       cu, scale, N, T, HK, HV, static_cast<uint8_t *>(ws), lay, o, sN, status);
 }
 
-template <typename Tin, bool kKeep>
-cudaError_t launch_d(int D, const void *v, const float *s0, const int32_t *cu, float scale, int N,
-                     int T, int HK, int HV, void *ws, float *o, float *sN, int *status,
+template <typename Tin, int D>
+cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float scale, int N, int T,
+                     int HK, int HV, void *ws, bool bwd, float *o, float *sN, int *status,
                      cudaStream_t s) {
-  if (D == 64)
-    return launch_nw<Tin, 64, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
-  if (D != 128) return cudaErrorInvalidValue;
+  const Layout lay = layout(N, T, HK, HV, D, bwd);
   // Two CTAs of four warps per head as long as they all run at once (one per SM): 4.9 us a chunk
   // with the read-out and 4.1 without it; the tcgen05 form of one CTA per head takes 4.9 and 5.3
   // us, this form with a whole head on eight warps 7.7.
-  if ((long long)N * HV * 2 <= 148)
-    return launch_nw<Tin, 128, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
-  return launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV,
-                             std::is_same<Tin, __half>::value ? KDA_F16 : KDA_BF16, ws, kKeep, o, sN,
-                             status, s);
+  if (D == 128 && (long long)N * HV * 2 > 148)
+    return launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV,
+                               std::is_same<Tin, __half>::value ? KDA_F16 : KDA_BF16, ws, bwd, o, sN,
+                               status, s);
+  if (bwd)
+    return launch_role<Tin, D, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
+  if (lay.seg_chunks) {
+    cudaError_t e =
+        launch_role<Tin, D, 4, kMap>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
+    if (e != cudaSuccess) return e;
+    auto scan = gdr_scan_kernel<D>;
+    const int bytes = 2 * D * D * 4;
+    e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    e = launch_behind(scan, dim3((unsigned)(N * HV)), 2 * D, bytes, s, cu, N, T, HV,
+                      static_cast<uint8_t *>(ws), lay, status);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_role<Tin, D, 4, kOut>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
 }
 
 }  // namespace
@@ -331,10 +487,10 @@ cudaError_t launch_gdr_state(const void *v, const float *s0, const int32_t *cu, 
                              int T, int HK, int HV, int D, kda_dtype dt, void *ws, bool bwd, float *o,
                              float *sN, int *status, cudaStream_t s) {
   if (dt == KDA_BF16)
-    return bwd ? launch_d<__nv_bfloat16, true>(D, v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s)
-               : launch_d<__nv_bfloat16, false>(D, v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
-  return bwd ? launch_d<__half, true>(D, v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s)
-             : launch_d<__half, false>(D, v, s0, cu, scale, N, T, HK, HV, ws, o, sN, status, s);
+    return D == 64 ? launch_d<__nv_bfloat16, 64>(v, s0, cu, scale, N, T, HK, HV, ws, bwd, o, sN, status, s)
+                   : launch_d<__nv_bfloat16, 128>(v, s0, cu, scale, N, T, HK, HV, ws, bwd, o, sN, status, s);
+  return D == 64 ? launch_d<__half, 64>(v, s0, cu, scale, N, T, HK, HV, ws, bwd, o, sN, status, s)
+                 : launch_d<__half, 128>(v, s0, cu, scale, N, T, HK, HV, ws, bwd, o, sN, status, s);
 }
 
 }  // namespace kda

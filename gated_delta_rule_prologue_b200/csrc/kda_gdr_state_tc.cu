@@ -164,6 +164,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
                     uint8_t *__restrict__ ws, Layout lay, float *__restrict__ o, float *sN,
                     int *status) {
   extern __shared__ uint8_t smem_raw[];
+  wait_for_previous_kernel();
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   Small &sm = *reinterpret_cast<Small *>(smem + 2 * kStage);
@@ -383,7 +384,6 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       }
     };
     if (warp == kChainWarps) {
-      wait_for_previous_kernel();
       load(0);
       if (chunks > 1) load(1);
     }

@@ -238,6 +238,18 @@ def test_chunk_forward_whole_head_ctas(kda):
     check_forward(p, CHUNK)
 
 
+@pytest.mark.parametrize("lens,HV,D,dtype", [([2000], 2, 128, BF16), ([2113], 1, 64, F16),
+                                             ([40, 1700, 0, 1100], 1, 128, F16),
+                                             ([3000, 2900], 2, 64, BF16)])
+@pytest.mark.parametrize("state", [True, False])
+def test_chunk_forward_in_segments(kda, lens, HV, D, dtype, state):
+    """Few long sequences: the state pass runs segments of them at once."""
+    p = Problem(lens, 1, HV, D, dtype, seed=sum(lens), state=state, decay="mixed")
+    p.g *= 0.3  # the slowest head's state outlives a segment
+    p.forward(kda.kda_gdr_chunk_fwd)
+    check_forward(p, CHUNK)
+
+
 @pytest.mark.parametrize("beta", [0.0, 1.0])
 def test_chunk_forward_beta_ends(kda, beta):
     p = Problem([100], 1, 2, 128, F16, seed=8, decay="none")
