@@ -114,9 +114,20 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
 
   float s[NT][4];
   zero(s);
-  const float *from = first == 0 ? (s0 ? s0 + nh * D * D : nullptr)
-                      : kRole == kOut ? reinterpret_cast<const float *>(ws + lay.seg_e) + seg * D * D
-                                      : nullptr;
+  auto store = [&](float *to) {
+    float *p = to + (size_t)row * D + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
+      *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
+    }
+  };
+  // The read-out of a cut sequence starts from the workspace alone, its first segment too: the last
+  // segment may be writing sN, which may be s0, by then.
+  const float *from = kRole == kOut && (first > 0 || (s0 && !is_last))
+                          ? reinterpret_cast<const float *>(ws + lay.seg_e) + seg * D * D
+                      : s0 && first == 0 ? s0 + nh * D * D
+                                         : nullptr;
   if (kRole == kMap && kind == 1) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -130,6 +141,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
       const float2 b = *reinterpret_cast<const float2 *>(p + 8 * D + 8 * i);
       s[i][0] = a.x; s[i][1] = a.y; s[i][2] = b.x; s[i][3] = b.y;
     }
+    if (kRole == kMap) store(reinterpret_cast<float *>(ws + lay.seg_e) + seg * D * D);
   }
 
   for (int c = first; c < end; ++c) {
@@ -321,14 +333,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   float *to = is_last && sN ? sN + nh * D * D : nullptr;
   if (kRole == kMap)
     to = reinterpret_cast<float *>(ws + (kind ? lay.seg_m : lay.seg_b)) + seg * D * D;
-  if (to) {
-    float *p = to + (size_t)row * D + col;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
-      *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
-    }
-  }
+  if (to) store(to);
 }
 
 // First states of the segments: E_1 = B_0 and E_g+1 = M_g E_g + B_g, one CTA per (sequence, head).

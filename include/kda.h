@@ -591,7 +591,10 @@ kda_status kda_gdr_decode_step(const void *q, const void *k, const void *v, cons
  * kda_gdr_recurrent.  Products run on the tensor cores on fp16 terms: q and k
  * exactly (bf16 values below 2^-14 of a 64-token tile's largest are off by up to
  * 2^-25 of it), every other operand as two terms of 11 bits each, so errors are
- * those of fp32 arithmetic relative to the largest values of a state row.
+ * those of fp32 arithmetic relative to the largest values of a state row.  A NaN or
+ * an infinity of a token reaches the earlier rows of its own 64-token chunk too, which
+ * are sums with it times zero; chunks before it, other heads and other sequences stay
+ * as they are, and so do other channels if it is one of v.
  */
 size_t kda_gdr_chunk_fwd_workspace_bytes(int N, int T, int HK, int HV, int D, kda_dtype dt);
 kda_status kda_gdr_chunk_fwd_ws(const void *q, const void *k, const void *v, const float *g,
