@@ -273,8 +273,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
       }
       float *op = o + ((size_t)t0 * HV + h) * D + row;
       const float q0 = a0.s * kqs.y, q1 = a1.s * kqs.y;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      auto out = [&](int i, auto whole) {
         const float2 g = *reinterpret_cast<const float2 *>(vec + kVecG * C + 8 * i + col);
         const float2 p = *reinterpret_cast<const float2 *>(vec + kVecP * C + 8 * i + col);
 #pragma unroll
@@ -282,8 +281,15 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
           const int t = 8 * i + col + (e & 1);
           const float gg = e & 1 ? g.y : g.x, pp = e & 1 ? p.y : p.x;
           const float x = gg * ((e >> 1 ? q1 : q0) * qs[i][e]) + (e >> 1 ? r1.s : r0.s) * pp * pu[i][e];
-          if (t < len) __stcs(op + (size_t)t * HV * D + 8 * (e >> 1), scale * x);
+          if (decltype(whole)::value || t < len) __stcs(op + (size_t)t * HV * D + 8 * (e >> 1), scale * x);
         }
+      };
+      if (len == C) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out(i, std::true_type{});
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out(i, std::false_type{});
       }
     }
     // S^T = G_C S^T + (E U)^T K.
