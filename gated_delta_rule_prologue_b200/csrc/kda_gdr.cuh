@@ -63,11 +63,11 @@ __host__ __device__ inline long long segment_slots(int N, int T, int L) {
   return (long long)T / ((long long)C * L) + N + 1;
 }
 // Chunks per segment (0: whole sequences), by a model of B200 measurements for sequences of about
-// T / N tokens: a chunk takes 4.9 us with the read-out and 4.1 without, one CTA of 64 value channels
-// runs per SM, a step of the scan takes 6 us, and the two more launches with their first loads 10.
-// Cutting has to save a tenth.  One prompt of 4096 tokens and 8 heads: 337 -> 166 us.
-inline int segment_chunks(int N, int T, int HV, int D) {
-  const long long ctas = (long long)N * HV * (D / 64);
+// T / N tokens: a chunk takes 4.9 us with the read-out and 4.4 without, one CTA per (segment, head) runs
+// per SM, a step of the scan takes 2.5 us, and the two more launches with their first loads 10.
+// Cutting has to save a tenth.
+inline int segment_chunks(int N, int T, int HV) {
+  const long long ctas = (long long)N * HV;
   if (N < 1 || T < 1 || ctas > 148) return 0;
   const long long n = (((long long)T + N - 1) / N + C - 1) / C;
   double best = 0.9 * 4.9 * (double)n;
@@ -76,8 +76,8 @@ inline int segment_chunks(int N, int T, int HV, int D) {
     const long long L = (n + G - 1) / G, Gs = (n + L - 1) / L;
     if (Gs < 2) continue;
     const long long maps = ctas * (2 * Gs - 3), reads = ctas * Gs;
-    const double t = (double)((maps + 147) / 148) * L * 4.1 + (double)((reads + 147) / 148) * L * 4.9 +
-                     6.0 * (double)(Gs - 2) + 10.0;
+    const double t = (double)((maps + 147) / 148) * L * 4.4 + (double)((reads + 147) / 148) * L * 4.9 +
+                     2.5 * (double)(Gs - 2) + 10.0;
     if (t < best) {
       best = t;
       len = (int)L;
@@ -85,6 +85,9 @@ inline int segment_chunks(int N, int T, int HV, int D) {
   }
   return len;
 }
+// M of a segment as the scan takes it: D rows of D fp16 hi and D fp16 lo (row_off), then the rows'
+// scales.  Row i has M's column i: the effect on the i-th unit vector.
+__host__ __device__ constexpr uint32_t map_bytes(int D) { return (uint32_t)D * D * 4 + D * 4; }
 
 // Byte offsets in the workspace.
 struct Layout {
@@ -92,7 +95,7 @@ struct Layout {
   size_t state, dstate, u, x;    // backward: per chunk fp32 S and dS' (key-major: [key][value channel]),
                                  // U and X [64][D]
   int seg_chunks;                // forward: chunks per segment, or 0
-  size_t seg_m, seg_b, seg_e;    // and per segment fp32 M, B and first state, each stored like a state
+  size_t seg_m, seg_b, seg_e;    // and per segment M (map_bytes), fp32 B and first state, like a state
   size_t bytes;
 };
 inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
@@ -106,10 +109,10 @@ inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
   l.u = l.dstate + (bwd ? sq : 0);
   l.x = l.u + (bwd ? rows : 0);
   l.seg_m = l.x + (bwd ? rows : 0);
-  l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV, D);
-  const size_t seg =
-      l.seg_chunks ? (size_t)segment_slots(N, T, l.seg_chunks) * HV * (size_t)D * D * 4 : 0;
-  l.seg_b = l.seg_m + seg;
+  l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV);
+  const size_t segs = l.seg_chunks ? (size_t)segment_slots(N, T, l.seg_chunks) * HV : 0;
+  const size_t seg = segs * D * D * 4;
+  l.seg_b = l.seg_m + segs * map_bytes(D);
   l.seg_e = l.seg_b + seg;
   l.bytes = l.seg_e + seg;
   return l;
@@ -172,6 +175,58 @@ __device__ __forceinline__ bool chunk_of_slot(const int32_t *cu, int N, int T, l
   if (cc < 0 || cc * C >= eos - bos) return false;
   c = (int)cc;
   return true;
+}
+
+// What a launch of the state pass is for.
+enum Role {
+  kOut,   // the read-out and the last states; of segments from the scan's states, if sequences are cut
+  kKeep,  // the backward's forward: S at the start of every chunk and U go to the workspace
+  kMap    // a segment's B (kind 0) or M (kind 1); not of a sequence's last segment, nor M of its first
+};
+// The chunks of a CTA of the state pass: first .. end - 1 of sequence n.
+struct Part {
+  int n, h, kind, bos, eos, first, end;
+  bool is_last;        // the sequence's last chunk is among them
+  size_t seg;          // the segment's (slot, head), if sequences are cut
+  long long slot;      // of the first chunk
+};
+// Part b (segments, or whole sequences, times heads; times two for maps); false: nothing to do.
+template <int kRole>
+__device__ __forceinline__ bool part_of(int b, const int32_t *cu, int N, int T, int HV, const Layout &lay,
+                                        int *status, Part &p) {
+  p.kind = kRole == kMap ? b & 1 : 0;
+  if (kRole == kMap) b >>= 1;
+  p.h = b % HV;
+  p.n = b / HV;
+  p.first = 0;
+  p.seg = 0;
+  const int L = kRole == kKeep ? 0 : lay.seg_chunks;
+  if (L == 0) {
+    seq_bounds(cu, p.n, T, status, p.bos, p.eos);
+    p.end = (p.eos - p.bos + C - 1) / C;
+  } else {
+    const long long slot = p.n;
+    const long long g = place_of_slot(cu, N, T, slot, C * L, status, p.n, p.bos, p.eos);
+    p.end = (p.eos - p.bos + C - 1) / C;
+    if (g < 0 || (g > 0 && g * L >= p.end) || !in_range(status, slot, segment_slots(N, T, L))) return false;
+    p.first = (int)g * L;
+    if (kRole == kMap && (p.first + L >= p.end || (p.kind == 1 && g == 0))) return false;
+    p.end = min(p.end, p.first + L);
+    p.seg = (size_t)slot * HV + p.h;
+  }
+  p.is_last = p.end * C >= p.eos - p.bos;
+  p.slot = first_slot(p.bos, p.n) + p.first;
+  return in_range(status, p.slot + (p.end - p.first), slots(N, T) + 1);
+}
+// Where a part's first state comes from (null: zero; a map of kind 1 starts from the identity).  The
+// read-out of a cut sequence starts from the workspace alone, its first segment too: the last
+// segment may be writing sN, which may be s0, by then.
+template <int kRole>
+__device__ __forceinline__ const float *first_state(const Part &p, const float *s0, const uint8_t *ws,
+                                                    const Layout &lay, int HV, int D) {
+  if (kRole == kOut && (p.first > 0 || (s0 && !p.is_last)))
+    return reinterpret_cast<const float *>(ws + lay.seg_e) + p.seg * D * D;
+  return s0 && p.first == 0 ? s0 + ((size_t)p.n * HV + p.h) * D * D : nullptr;
 }
 
 // ---------------------------------------------------------------------------
@@ -367,8 +422,8 @@ __device__ __forceinline__ void split_rows_in_place(uint8_t *base, int row0, int
 
 // Host side (kda_gdr_*.cu), called by kda_api.cu; the *_tc form is launch_gdr_state's for D = 128.
 cudaError_t launch_gdr_state_tc(const void *v, const float *s0, const int32_t *cu, float scale, int N,
-                                int T, int HK, int HV, kda_dtype dt, void *ws, bool bwd, float *o,
-                                float *sN, int *status, cudaStream_t s);
+                                int T, int HK, int HV, kda_dtype dt, void *ws, gdr::Role role,
+                                float *o, float *sN, int *status, cudaStream_t s);
 cudaError_t launch_gdr_prep(const void *q, const void *k, const float *g, const float *beta,
                             const int32_t *cu, int N, int T, int HK, int HV, int D, kda_dtype dt,
                             void *ws, bool bwd, int *status, cudaStream_t s);

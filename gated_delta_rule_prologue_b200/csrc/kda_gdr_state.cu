@@ -35,6 +35,14 @@ template <int D, int NW> struct StateSmem {
   static constexpr uint32_t kBytes = 2 * kStage;
 };
 
+// Two stages of a segment's M and of 64 value channels of its B.
+template <int D> struct ScanSmem {
+  static constexpr int kLd = D + 8;                            // floats per row of B
+  static constexpr uint32_t kB = map_bytes(D);
+  static constexpr uint32_t kStage = kB + 64 * kLd * 4;
+  static constexpr uint32_t kBytes = 2 * kStage;
+};
+
 // Byte offset of the 16-byte piece p of token row `row` of a V tile 16 NW channels wide.
 template <int NW> __device__ __forceinline__ uint32_t v_off(int row, int p) {
   return (uint32_t)(row * (32 * NW) + ((p ^ (row & 7)) << 4));
@@ -46,13 +54,6 @@ __device__ __forceinline__ float2 widen2(uint32_t u, __nv_bfloat16) {
 __device__ __forceinline__ float2 widen2(uint32_t u, __half) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
-
-// What a launch of the pass is for.
-enum Role {
-  kOut,   // the read-out and the last states; of segments from the scan's states, if sequences are cut
-  kKeep,  // the backward's forward: S at the start of every chunk and U go to the workspace
-  kMap    // a segment's B (kind 0) or M (kind 1); not of a sequence's last segment, nor M of its first
-};
 
 template <typename Tin, int D, int NW, int kRole>
 __global__ void __launch_bounds__(NW * 32, 1)
@@ -69,29 +70,10 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   int b = blockIdx.x;
   const int part = b % kParts;
   b /= kParts;
-  const int kind = kRole == kMap ? b & 1 : 0;
-  if (kRole == kMap) b >>= 1;
-  const int h = b % HV, hk = h / (HV / HK);
-  int n = b / HV, bos, eos, first = 0, end;   // chunks first .. end - 1 of sequence n
-  const int L = kRole == kKeep ? 0 : lay.seg_chunks;
-  size_t seg = 0;                             // the segment's (slot, head)
-  if (L == 0) {
-    seq_bounds(cu, n, T, status, bos, eos);
-    end = (eos - bos + C - 1) / C;
-  } else {
-    const long long slot = n;
-    const long long g = place_of_slot(cu, N, T, slot, C * L, status, n, bos, eos);
-    end = (eos - bos + C - 1) / C;
-    if (g < 0 || (g > 0 && g * L >= end) || !in_range(status, slot, segment_slots(N, T, L))) return;
-    first = (int)g * L;
-    if (kRole == kMap && (first + L >= end || (kind == 1 && g == 0))) return;
-    end = min(end, first + L);
-    seg = (size_t)slot * HV + h;
-  }
-  const bool is_last = end * C >= eos - bos;
-  const long long slot0 = first_slot(bos, n);
-  if (!in_range(status, slot0 + end, slots(N, T) + 1)) return;
-  const size_t nh = (size_t)n * HV + h;
+  Part pt;
+  if (!part_of<kRole>(b, cu, N, T, HV, lay, status, pt)) return;
+  const int h = pt.h, hk = h / (HV / HK), bos = pt.bos, eos = pt.eos, first = pt.first, end = pt.end;
+  const long long slot0 = pt.slot - first;
   const int ch0 = (part * NW + warp) * 16;     // the warp's first value channel
   const int row = ch0 + lane / 4;              // and this lane's rows: row, row + 8
   const int col = 2 * (lane & 3);
@@ -122,13 +104,8 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
       *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
     }
   };
-  // The read-out of a cut sequence starts from the workspace alone, its first segment too: the last
-  // segment may be writing sN, which may be s0, by then.
-  const float *from = kRole == kOut && (first > 0 || (s0 && !is_last))
-                          ? reinterpret_cast<const float *>(ws + lay.seg_e) + seg * D * D
-                      : s0 && first == 0 ? s0 + nh * D * D
-                                         : nullptr;
-  if (kRole == kMap && kind == 1) {
+  const float *from = first_state<kRole>(pt, s0, ws, lay, HV, D);
+  if (kRole == kMap && pt.kind == 1) {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -141,7 +118,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
       const float2 b = *reinterpret_cast<const float2 *>(p + 8 * D + 8 * i);
       s[i][0] = a.x; s[i][1] = a.y; s[i][2] = b.x; s[i][3] = b.y;
     }
-    if (kRole == kMap) store(reinterpret_cast<float *>(ws + lay.seg_e) + seg * D * D);
+    if (kRole == kMap) store(reinterpret_cast<float *>(ws + lay.seg_e) + pt.seg * D * D);
   }
 
   for (int c = first; c < end; ++c) {
@@ -204,7 +181,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
           const float2 g = *reinterpret_cast<const float2 *>(vec + kVecG * C + 8 * i + col);
           const float2 bt = *reinterpret_cast<const float2 *>(vec + kVecBeta * C + 8 * i + col);
           float2 v0 = widen2(b[2 * e], Tin{}), v1 = widen2(b[2 * e + 1], Tin{});
-          if (kRole == kMap && kind == 1) v0 = v1 = make_float2(0.f, 0.f);
+          if (kRole == kMap && pt.kind == 1) v0 = v1 = make_float2(0.f, 0.f);
           ks[i][0] = bt.x * (v0.x - g.x * (f0 * ks[i][0]));
           ks[i][1] = bt.y * (v0.y - g.y * (f0 * ks[i][1]));
           ks[i][2] = bt.x * (v1.x - g.x * (f1 * ks[i][2]));
@@ -336,43 +313,69 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   cp_wait<0>();
   next_kernel_may_start();
 
-  float *to = is_last && sN ? sN + nh * D * D : nullptr;
-  if (kRole == kMap)
-    to = reinterpret_cast<float *>(ws + (kind ? lay.seg_m : lay.seg_b)) + seg * D * D;
-  if (to) store(to);
+  if (kRole == kMap && pt.kind == 1) {
+    uint8_t *m = ws + lay.seg_m + pt.seg * map_bytes(D);
+    Scale r0, r1;
+    row_scales(s, r0, r1);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        uint32_t hi, lo;
+        split2(s[i][2 * e], s[i][2 * e + 1], e ? r1.inv : r0.inv, hi, lo);
+        uint8_t *to = m + row_off<D>(row + 8 * e, i) + 2 * col;
+        *reinterpret_cast<uint32_t *>(to) = hi;
+        *reinterpret_cast<uint32_t *>(to + 2 * D) = lo;
+      }
+    if ((lane & 3) == 0) {
+      float *scales = reinterpret_cast<float *>(m + D * D * 4);
+      scales[row] = r0.s;
+      scales[row + 8] = r1.s;
+    }
+  } else if (kRole == kMap) {
+    store(reinterpret_cast<float *>(ws + lay.seg_b) + pt.seg * D * D);
+  } else if (pt.is_last && sN) {
+    store(sN + ((size_t)pt.n * HV + h) * D * D);
+  }
 }
 
-// First states of the segments: E_1 = B_0 and E_g+1 = M_g E_g + B_g, one CTA per (sequence, head).
+// First states of the segments: E_1 = B_0 and E_g+1 = M_g E_g + B_g, 64 value channels per CTA.
 // E^T is the A operand of its own next step, as S^T in the pass above: a warp owns 16 value channels.
-// M (rows: its columns) is split in its place with one power of two, two matrices in shared memory.
+// M comes split, row by row; its rows' scales go to E's columns.
 template <int D>
-__global__ void __launch_bounds__(2 * D, 1)
+__global__ void __launch_bounds__(128, 1)
 gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *__restrict__ ws,
                 Layout lay, int *status) {
-  constexpr int NT = D / 8, KK = D / 16, kWarps = D / 16, kThreads = 2 * D;
+  using Sm = ScanSmem<D>;
+  constexpr int NT = D / 8, KK = D / 16, kParts = D / 64;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float largest[kWarps];
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = blockIdx.x / HV, h = blockIdx.x % HV, L = lay.seg_chunks;
+  const int part = blockIdx.x % kParts, nh = blockIdx.x / kParts;
+  const int n = nh / HV, h = nh % HV, L = lay.seg_chunks;
   int bos, eos;
   seq_bounds(cu, n, T, status, bos, eos);
   const int G = ((eos - bos + C - 1) / C + L - 1) / L;
   const long long slot0 = bos / (C * L) + n;
   if (G < 2 || !in_range(status, slot0 + G, segment_slots(N, T, L) + 1)) return;
-  const int row = 16 * warp + lane / 4, col = 2 * (lane & 3);
-  auto block_of = [&](size_t area, int g) {
+  const int rl = 16 * warp + lane / 4, row = 64 * part + rl, col = 2 * (lane & 3);
+  auto state_of = [&](size_t area, int g) {
     return reinterpret_cast<float *>(ws + area) + ((size_t)(slot0 + g) * HV + h) * D * D;
   };
   auto fetch = [&](int g) {
-    cp_block(smem_addr(smem) + (g & 1) * D * D * 4, reinterpret_cast<const uint8_t *>(block_of(lay.seg_m, g)),
-             D * D * 4);
+    const uint32_t st = smem_addr(smem) + (g & 1) * Sm::kStage;
+    cp_block(st, ws + lay.seg_m + ((size_t)(slot0 + g) * HV + h) * map_bytes(D), map_bytes(D));
+    const float *b = state_of(lay.seg_b, g) + 64 * part * D;
+    for (int i = threadIdx.x; i < 64 * D / 4; i += 128) {
+      const int r = i / (D / 4), p = i % (D / 4);
+      cp16(st + Sm::kB + (r * Sm::kLd + 4 * p) * 4, b + r * D + 4 * p);
+    }
   };
   if (G > 2) fetch(1);
   cp_commit();
   float s[NT][4];
   {
-    const float *p = block_of(lay.seg_b, 0) + (size_t)row * D + col;
+    const float *p = state_of(lay.seg_b, 0) + (size_t)row * D + col;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const float2 a = *reinterpret_cast<const float2 *>(p + 8 * i);
@@ -381,7 +384,7 @@ gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *_
     }
   }
   for (int g = 1;; ++g) {
-    float *p = block_of(lay.seg_e, g) + (size_t)row * D + col;
+    float *p = state_of(lay.seg_e, g) + (size_t)row * D + col;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
@@ -392,28 +395,20 @@ gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *_
     cp_commit();
     cp_wait<1>();
     __syncthreads();
-    uint8_t *mat = smem + (g & 1) * D * D * 4;
-    float big = 0.f;
-    for (int i = threadIdx.x; i < D * D / 4; i += kThreads) {
-      const float4 x = reinterpret_cast<const float4 *>(mat)[i];
-      big = fmaxf(fmaxf(fmaxf(big, fabsf(x.x)), fmaxf(fabsf(x.y), fabsf(x.z))), fabsf(x.w));
+    const uint8_t *st = smem + (g & 1) * Sm::kStage;
+    const uint32_t mat = smem_addr(st);
+    const float *scales = reinterpret_cast<const float *>(st + D * D * 4) + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float2 f = *reinterpret_cast<const float2 *>(scales + 8 * i);
+      s[i][0] *= f.x; s[i][1] *= f.y; s[i][2] *= f.x; s[i][3] *= f.y;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-    if (lane == 0) largest[warp] = big;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) big = fmaxf(big, largest[i]);
-    const Scale ms = scale_of(big);
-    split_rows_in_place<D>(mat, 16 * warp, 16, ms.inv);
     Scale a0, a1;
     row_scales(s, a0, a1);
     uint32_t hi[KK][4], lo[KK][4];
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) split_a(s, kk, a0, a1, hi[kk], lo[kk]);
-    __syncthreads();
-    const float f0 = ms.s * a0.s, f1 = ms.s * a1.s;
-    const float *bp = block_of(lay.seg_b, g) + (size_t)row * D + col;
+    const float *bp = reinterpret_cast<const float *>(st + Sm::kB) + rl * Sm::kLd + col;
 #pragma unroll
     for (int j = 0; j < NT / 4; ++j) {
       float acc[4][4];
@@ -423,8 +418,8 @@ gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *_
 #pragma unroll
         for (int np = 0; np < 2; ++np) {
           uint32_t b[4], bl[4];
-          load_rows_bt<D>(b, smem_addr(mat), 32 * j + 16 * np, 16 * kk, false);
-          load_rows_bt<D>(bl, smem_addr(mat), 32 * j + 16 * np, 16 * kk, true);
+          load_rows_bt<D>(b, mat, 32 * j + 16 * np, 16 * kk, false);
+          load_rows_bt<D>(bl, mat, 32 * j + 16 * np, 16 * kk, true);
           mma(acc[2 * np], hi[kk], b[0], b[1]);
           mma(acc[2 * np + 1], hi[kk], b[2], b[3]);
           mma(acc[2 * np], lo[kk], b[0], b[1]);
@@ -435,12 +430,12 @@ gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *_
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float2 x = *reinterpret_cast<const float2 *>(bp + 32 * j + 8 * i);
-        const float2 y = *reinterpret_cast<const float2 *>(bp + 8 * D + 32 * j + 8 * i);
+        const float2 y = *reinterpret_cast<const float2 *>(bp + 8 * Sm::kLd + 32 * j + 8 * i);
         float(&t)[4] = s[4 * j + i];
-        t[0] = fmaf(f0, acc[i][0], x.x);
-        t[1] = fmaf(f0, acc[i][1], x.y);
-        t[2] = fmaf(f1, acc[i][2], y.x);
-        t[3] = fmaf(f1, acc[i][3], y.y);
+        t[0] = fmaf(a0.s, acc[i][0], x.x);
+        t[1] = fmaf(a0.s, acc[i][1], x.y);
+        t[2] = fmaf(a1.s, acc[i][2], y.x);
+        t[3] = fmaf(a1.s, acc[i][3], y.y);
       }
     }
     __syncthreads();  // the matrix has been read: the next fetch may take its place
@@ -468,28 +463,33 @@ cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float sc
                      int HK, int HV, void *ws, bool bwd, float *o, float *sN, int *status,
                      cudaStream_t s) {
   const Layout lay = layout(N, T, HK, HV, D, bwd);
-  // Two CTAs of four warps per head as long as they all run at once (one per SM): 4.9 us a chunk
-  // with the read-out and 4.1 without it; the tcgen05 form of one CTA per head takes 4.9 and 5.3
-  // us, this form with a whole head on eight warps 7.7.
-  if (D == 128 && (long long)N * HV * 2 > 148)
-    return launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV,
-                               std::is_same<Tin, __half>::value ? KDA_F16 : KDA_BF16, ws, bwd, o, sN,
-                               status, s);
+  // D = 128: two CTAs of four warps per head, one per SM, if they all run at once, or else, and for
+  // segments, which fill the SMs by themselves, the tcgen05 form with one CTA per head.  A chunk takes
+  // 4.9 us in either with the read-out; without it 4.1 us here and 4.4 (maps) and 5.3 us (kept) there.
+  const bool tensor_memory = D == 128 && (lay.seg_chunks || (long long)N * HV * 2 > 148);
+  const kda_dtype dt = std::is_same<Tin, __half>::value ? KDA_F16 : KDA_BF16;
   if (bwd)
-    return launch_role<Tin, D, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
+    return tensor_memory
+               ? launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, kKeep, o, sN, status, s)
+               : launch_role<Tin, D, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
   if (lay.seg_chunks) {
-    cudaError_t e =
-        launch_role<Tin, D, 4, kMap>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
+    cudaError_t e;
+    if constexpr (D == 128)
+      e = launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, kMap, o, sN, status, s);
+    else
+      e = launch_role<Tin, D, 4, kMap>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
     if (e != cudaSuccess) return e;
     auto scan = gdr_scan_kernel<D>;
-    const int bytes = 2 * D * D * 4;
+    const int bytes = (int)ScanSmem<D>::kBytes;
     e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    e = launch_behind(scan, dim3((unsigned)(N * HV)), 2 * D, bytes, s, cu, N, T, HV,
+    e = launch_behind(scan, dim3((unsigned)(N * HV * (D / 64))), 128, bytes, s, cu, N, T, HV,
                       static_cast<uint8_t *>(ws), lay, status);
     if (e != cudaSuccess) return e;
   }
-  return launch_role<Tin, D, 4, kOut>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
+  return tensor_memory
+             ? launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, kOut, o, sN, status, s)
+             : launch_role<Tin, D, 4, kOut>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
 }
 
 }  // namespace

@@ -155,9 +155,7 @@ bool make_v_map(CUtensorMap *m, const void *v, kda_dtype dt, int HV, int T) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// kKeep: the backward's forward: S at the start of every chunk (as [key channel][value channel])
-// and U go to the workspace, and there is no read-out.
-template <typename Tin, bool kKeep>
+template <typename Tin, int kRole>
 __global__ void __launch_bounds__(kThreads, 1)
 gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
                     const int32_t *__restrict__ cu, float scale, int N, int T, int HK, int HV,
@@ -169,18 +167,19 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
                                               ~static_cast<uintptr_t>(1023));
   Small &sm = *reinterpret_cast<Small *>(smem + 2 * kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nh = blockIdx.x, n = nh / HV, h = nh % HV, hk = h / (HV / HK);
-  int bos, eos;
-  seq_bounds(cu, n, T, status, bos, eos);
-  const int chunks = (eos - bos + C - 1) / C;
-  const long long slot0 = first_slot(bos, n);
-  if (!in_range(status, slot0 + chunks, slots(N, T) + 1)) return;
+  Part pt;
+  if (!part_of<kRole>(blockIdx.x, cu, N, T, HV, lay, status, pt)) return;
+  const int h = pt.h, hk = h / (HV / HK);
+  const int bos = pt.bos + pt.first * C, eos = pt.eos, chunks = pt.end - pt.first;  // of this part
+  const long long slot0 = pt.slot;
+  const size_t nh = (size_t)pt.n * HV + h;
+  const bool identity = kRole == kMap && pt.kind == 1;  // M: from the identity, without values
 
   if (chunks == 0) {  // the state comes back as it was
     if (sN)
       for (int i = tid; i < D * D / 4; i += kThreads)
-        reinterpret_cast<float4 *>(sN + (size_t)nh * D * D)[i] =
-            s0 ? reinterpret_cast<const float4 *>(s0 + (size_t)nh * D * D)[i]
+        reinterpret_cast<float4 *>(sN + nh * D * D)[i] =
+            s0 ? reinterpret_cast<const float4 *>(s0 + nh * D * D)[i]
                : make_float4(0.f, 0.f, 0.f, 0.f);
     return;
   }
@@ -241,16 +240,25 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       return fmaxf(x, most[half ^ 1][lane]);
     };
     float s[D / 2];  // key channels 64 half ..
-    if (s0) {
-      const float4 *p = reinterpret_cast<const float4 *>(s0 + ((size_t)nh * D + row) * D + half * 64);
+    const size_t at = (size_t)row * D + half * 64;
+    auto store = [&](float *to) {
+      float4 *p = reinterpret_cast<float4 *>(to + at);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        p[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+    };
+    const float *from = first_state<kRole>(pt, s0, ws, lay, HV, D);
+    if (from && !identity) {
+      const float4 *p = reinterpret_cast<const float4 *>(from + at);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         const float4 x = p[i];
         s[4 * i] = x.x; s[4 * i + 1] = x.y; s[4 * i + 2] = x.z; s[4 * i + 3] = x.w;
       }
+      if (kRole == kMap) store(reinterpret_cast<float *>(ws + lay.seg_e) + pt.seg * D * D);
     } else {
 #pragma unroll
-      for (int i = 0; i < D / 2; ++i) s[i] = 0.f;
+      for (int i = 0; i < D / 2; ++i) s[i] = identity && row == 64 * half + i ? 1.f : 0.f;
     }
     for (int c = 0; c < chunks; ++c) {
       const uint32_t par = c & 1;
@@ -269,7 +277,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       if (half == 0) sm.s_scale[par][row] = ss.s;
       tmem_wait_st();
       warp_arrive(&sm.s_ready);
-      if constexpr (kKeep) {
+      if constexpr (kRole == kKeep) {
         float *p = reinterpret_cast<float *>(ws + lay.state) +
                    (((size_t)(slot0 + c) * HV + h) * D + half * 64) * D + row;
 #pragma unroll
@@ -278,7 +286,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       if (!(ok = wait(&sm.full[par], (c >> 1) & 1, sm, status))) break;
       if (warp == 0) {
         if (!(ok = wait(&sm.s_ready, par, sm, status))) break;
-        constexpr uint32_t id = tc::idesc_fp16(128, kKeep ? 64 : 128, false, false);
+        constexpr uint32_t id = tc::idesc_fp16(128, kRole == kOut ? 128 : 64, false, false);
         const uint64_t b0 = tc::sdesc(st32 + kStKq, 16, 1024);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
@@ -290,7 +298,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       }
       const float ks = *reinterpret_cast<const float *>(st + kStScales);
       const float gl = vec[kVecG * C + C - 1];
-      if (len < 32) {  // other sequences' rows: this thread alone reads this column
+      if (len < 32 && !identity) {  // other sequences' rows: this thread alone reads this column
         for (int t = max(len, 0); t < 32; ++t) const_cast<Tin *>(vt)[t * D] = from_f32<Tin>(0.f);
       }
       float x[32];
@@ -298,7 +306,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
         const float f = -ss.s * ks;
         float bb[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) bb[i] = to_f32(vt[i * D]);  // on their way while the MMAs run
+        for (int i = 0; i < 32; ++i) bb[i] = identity ? 0.f : to_f32(vt[i * D]);  // on their way while the MMAs run
         if (!(ok = wait(&sm.d_s, par, sm, status))) break;
         tc::tmem_ld32(tl + TM_ACC + 32 * half, x);
 #pragma unroll
@@ -321,7 +329,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       if (warp == 0) {
         if (!(ok = wait(&sm.r_ready, par, sm, status))) break;
         // the last chunk's U has been read
-        if (c > 0 && !(ok = wait(&sm.u_ready, par ^ 1, sm, status))) break;
+        if (kRole != kMap && c > 0 && !(ok = wait(&sm.u_ready, par ^ 1, sm, status))) break;
         mma_triangular(tm + TM_U, tm + TM_W, tc::sdesc(st32 + kStTp + kT_HI, 16, 1024));
         commit(leader, &sm.d_u);
       }
@@ -345,7 +353,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       if (warp == 0) {
         if (!(ok = wait(&sm.w_ready, par, sm, status))) break;
         // the accumulator lies over Q S
-        if (!kKeep && !(ok = wait(&sm.q_read, par, sm, status))) break;
+        if (kRole == kOut && !(ok = wait(&sm.q_read, par, sm, status))) break;
         constexpr uint32_t id = tc::idesc_fp16(128, 128, false, true);
         const uint64_t b0 = tc::sdesc(st32 + kStKq, kKq * 128, 1024);
 #pragma unroll
@@ -365,11 +373,24 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
         for (int i = 0; i < 32; ++i) s[32 * b + i] = fmaf(gl, s[32 * b + i], f * x[i]);
       }
     }
-    if (ok && sN) {
-      float4 *p = reinterpret_cast<float4 *>(sN + ((size_t)nh * D + row) * D + half * 64);
+    if (kRole == kOut && ok && pt.is_last && sN) store(sN + nh * D * D);
+    if (kRole == kMap && ok && !identity) store(reinterpret_cast<float *>(ws + lay.seg_b) + pt.seg * D * D);
+    if (identity && ok) {
+      const float big = meet(0, max_abs32(s + 32, max_abs32(s, 0.f)), chunks & 1);
+      const Scale sc = scale_of(big);
+      uint8_t *m = ws + lay.seg_m + pt.seg * map_bytes(D);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        p[i] = make_float4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
+      for (int i = 0; i < 8; ++i) {
+        uint4 hi, lo;
+        split2(s[8 * i], s[8 * i + 1], sc.inv, hi.x, lo.x);
+        split2(s[8 * i + 2], s[8 * i + 3], sc.inv, hi.y, lo.y);
+        split2(s[8 * i + 4], s[8 * i + 5], sc.inv, hi.z, lo.z);
+        split2(s[8 * i + 6], s[8 * i + 7], sc.inv, hi.w, lo.w);
+        uint8_t *to = m + row_off<D>(row, 8 * half + i);
+        *reinterpret_cast<uint4 *>(to) = hi;
+        *reinterpret_cast<uint4 *>(to + 2 * D) = lo;
+      }
+      if (half == 0) reinterpret_cast<float *>(m + D * D * 4)[row] = sc.s;
     }
   } else {
     auto load = [&](int c) {
@@ -377,10 +398,10 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       const long long slot = slot0 + c;
       uint64_t *bar = &sm.full[c & 1];
       if (lane == 0) {
-        tc::mbar_arrive_expect_tx(bar, kq_bytes(D) + kTpBytes + C * D * 2);
+        tc::mbar_arrive_expect_tx(bar, kq_bytes(D) + kTpBytes + (identity ? 0 : C * D * 2));
         tc::bulk_load(st, ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D), kq_bytes(D), bar);
         tc::bulk_load(st + kStTp, ws + lay.tp + (size_t)(slot * HV + h) * kTpBytes, kTpBytes, bar);
-        tc::tma_load_2d(st + kStV, &tm_v, bar, h * D, bos + c * C);
+        if (!identity) tc::tma_load_2d(st + kStV, &tm_v, bar, h * D, bos + c * C);
       }
     };
     if (warp == kChainWarps) {
@@ -392,6 +413,12 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       const uint8_t *st = smem + par * kStage;
       const float *vec = reinterpret_cast<const float *>(st + kStTp + kVec);
       const int t0 = bos + c * C, len = min(C, eos - t0);
+      if constexpr (kRole == kMap) {  // nothing to read out: a stage is free when the chain has left it
+        if (warp > kChainWarps) break;
+        if (!(ok = wait(&sm.s_ready, par, sm, status))) break;
+        if (c > 0 && c + 1 < chunks) load(c + 1);
+        continue;
+      }
       if (!(ok = wait(&sm.full[par], (c >> 1) & 1, sm, status))) break;
       if (!(ok = wait(&sm.s_ready, par, sm, status))) break;
       // Chunk c - 1's read-out is done, and with it every reader of its stage.
@@ -399,8 +426,8 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
         if (!(ok = wait(&sm.out_done, par ^ 1, sm, status))) break;
         if (c + 1 < chunks) load(c + 1);
       }
-      float q[kKeep ? 1 : C];
-      if constexpr (!kKeep) {
+      float q[kRole == kOut ? C : 1];
+      if constexpr (kRole == kOut) {
         const float qf = sm.s_scale[par][row] * *reinterpret_cast<const float *>(st + kStScales + 4);
         if (!(ok = wait(&sm.d_s, par, sm, status))) break;
 #pragma unroll
@@ -427,7 +454,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
           x[i + 3] *= rf * tt.w;
         }
       };
-      if constexpr (kKeep) {
+      if constexpr (kRole == kKeep) {
         float *p = reinterpret_cast<float *>(ws + lay.u) + ((size_t)(slot0 + c) * HV + h) * C * D + row;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -500,31 +527,37 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
   if (warp == 0) tc::tmem_dealloc(tm, 512);
 }
 
-template <typename Tin, bool kKeep>
+template <typename Tin, int kRole>
 cudaError_t launch_typed(const void *v, const float *s0, const int32_t *cu, float scale, int N, int T,
                          int HK, int HV, kda_dtype dt, void *ws, float *o, float *sN, int *status,
                          cudaStream_t s) {
-  auto kern = gdr_state_tc_kernel<Tin, kKeep>;
+  auto kern = gdr_state_tc_kernel<Tin, kRole>;
   const cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
   if (e != cudaSuccess) return e;
-  const long long ctas = (long long)N * HV;
+  const Layout lay = layout(N, T, HK, HV, D, kRole == kKeep);
+  const long long units = lay.seg_chunks ? segment_slots(N, T, lay.seg_chunks) : N;
+  const long long ctas = units * HV * (kRole == kMap ? 2 : 1);
   CUtensorMap tm;
   if (ctas >= (1LL << 31) || !make_v_map(&tm, v, dt, HV, T)) return cudaErrorInvalidValue;
   return launch_behind(kern, dim3((unsigned)ctas), kThreads, kSmem, s, tm, s0, cu, scale, N, T, HK, HV,
-                       static_cast<uint8_t *>(ws), layout(N, T, HK, HV, D, kKeep), o, sN, status);
+                       static_cast<uint8_t *>(ws), lay, o, sN, status);
+}
+
+template <typename Tin, typename... Args> cudaError_t launch_for(Role role, Args... args) {
+  return role == kOut    ? launch_typed<Tin, kOut>(args...)
+         : role == kKeep ? launch_typed<Tin, kKeep>(args...)
+                         : launch_typed<Tin, kMap>(args...);
 }
 
 }  // namespace
 
 cudaError_t launch_gdr_state_tc(const void *v, const float *s0, const int32_t *cu, float scale, int N,
-                                int T, int HK, int HV, kda_dtype dt, void *ws, bool bwd, float *o,
+                                int T, int HK, int HV, kda_dtype dt, void *ws, Role role, float *o,
                                 float *sN, int *status, cudaStream_t s) {
-  if (dt == KDA_BF16)
-    return bwd ? launch_typed<__nv_bfloat16, true>(v, s0, cu, scale, N, T, HK, HV, dt, ws, o, sN, status, s)
-               : launch_typed<__nv_bfloat16, false>(v, s0, cu, scale, N, T, HK, HV, dt, ws, o, sN, status, s);
-  return bwd ? launch_typed<__half, true>(v, s0, cu, scale, N, T, HK, HV, dt, ws, o, sN, status, s)
-             : launch_typed<__half, false>(v, s0, cu, scale, N, T, HK, HV, dt, ws, o, sN, status, s);
+  return dt == KDA_BF16
+             ? launch_for<__nv_bfloat16>(role, v, s0, cu, scale, N, T, HK, HV, dt, ws, o, sN, status, s)
+             : launch_for<__half>(role, v, s0, cu, scale, N, T, HK, HV, dt, ws, o, sN, status, s);
 }
 
 }  // namespace kda
