@@ -63,21 +63,24 @@ __host__ __device__ inline long long segment_slots(int N, int T, int L) {
   return (long long)T / ((long long)C * L) + N + 1;
 }
 // Chunks per segment (0: whole sequences), by a model of B200 measurements for sequences of about
-// T / N tokens: a chunk takes 4.9 us with the read-out and 4.4 without, one CTA per (segment, head) runs
-// per SM, a step of the scan takes 2.5 us, and the two more launches with their first loads 10.
-// Cutting has to save a tenth.
-inline int segment_chunks(int N, int T, int HV) {
+// T / N tokens, one CTA per (segment, head) and SM.  Microseconds for D = 128 (64): a chunk 4.9 (3.5)
+// of whole sequences, 4.2 (2.2) of a map, 5.3 (3.5) of a segment's read-out, a wave of either 3 more,
+// a step of the scan 2 (0.9), the two more launches 13 (4).  Cutting has to save a tenth.
+inline int segment_chunks(int N, int T, int HV, int D) {
   const long long ctas = (long long)N * HV;
   if (N < 1 || T < 1 || ctas > 148) return 0;
+  const bool d128 = D == 128;
+  const double whole = d128 ? 4.9 : 3.5, map = d128 ? 4.2 : 2.2, read = d128 ? 5.3 : 3.5;
+  const double step = d128 ? 2.0 : 0.9, more = d128 ? 13.0 : 4.0;
   const long long n = (((long long)T + N - 1) / N + C - 1) / C;
-  double best = 0.9 * 4.9 * (double)n;
+  double best = 0.9 * whole * (double)n;
   int len = 0;
   for (long long G = 2; G <= n / 2 && G <= 64; ++G) {
     const long long L = (n + G - 1) / G, Gs = (n + L - 1) / L;
     if (Gs < 2) continue;
     const long long maps = ctas * (2 * Gs - 3), reads = ctas * Gs;
-    const double t = (double)((maps + 147) / 148) * L * 4.4 + (double)((reads + 147) / 148) * L * 4.9 +
-                     2.5 * (double)(Gs - 2) + 10.0;
+    const double t = (double)((maps + 147) / 148) * (L * map + 3.0) +
+                     (double)((reads + 147) / 148) * (L * read + 3.0) + step * (double)(Gs - 2) + more;
     if (t < best) {
       best = t;
       len = (int)L;
@@ -109,7 +112,7 @@ inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
   l.u = l.dstate + (bwd ? sq : 0);
   l.x = l.u + (bwd ? rows : 0);
   l.seg_m = l.x + (bwd ? rows : 0);
-  l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV);
+  l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV, D);
   const size_t segs = l.seg_chunks ? (size_t)segment_slots(N, T, l.seg_chunks) * HV : 0;
   const size_t seg = segs * D * D * 4;
   l.seg_b = l.seg_m + segs * map_bytes(D);

@@ -35,12 +35,16 @@ template <int D, int NW> struct StateSmem {
   static constexpr uint32_t kBytes = 2 * kStage;
 };
 
-// Two stages of a segment's M and of 64 value channels of its B.
+// Value channels of a scan's CTA, and its shared memory: two stages of a segment's M and of those
+// channels of its B, and the halves of E that its warps exchange.
+constexpr int kScanRows = 32;
 template <int D> struct ScanSmem {
-  static constexpr int kLd = D + 8;                            // floats per row of B
+  static constexpr int kLd = D + 8;                            // floats per row of B and E
+  static constexpr uint32_t kRows = kScanRows * kLd * 4;
   static constexpr uint32_t kB = map_bytes(D);
-  static constexpr uint32_t kStage = kB + 64 * kLd * 4;
-  static constexpr uint32_t kBytes = 2 * kStage;
+  static constexpr uint32_t kStage = kB + kRows;
+  static constexpr uint32_t kE = 2 * kStage;
+  static constexpr uint32_t kBytes = kE + kRows;
 };
 
 // Byte offset of the 16-byte piece p of token row `row` of a V tile 16 NW channels wide.
@@ -339,15 +343,17 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   }
 }
 
-// First states of the segments: E_1 = B_0 and E_g+1 = M_g E_g + B_g, 64 value channels per CTA.
-// E^T is the A operand of its own next step, as S^T in the pass above: a warp owns 16 value channels.
-// M comes split, row by row; its rows' scales go to E's columns.
+// First states of the segments: E_1 = B_0 and E_g+1 = M_g E_g + B_g, 32 value channels per CTA.
+// E^T is the A operand of its own next step, as S^T in the pass above.  Four warps: 16 value channels
+// times half the key channels of the result each, and the halves are exchanged after every step.  M
+// comes split, row by row; its rows' scales go to E's columns.
+// Bound: a step's chain; 192 MMAs a warp.
 template <int D>
 __global__ void __launch_bounds__(128, 1)
 gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *__restrict__ ws,
                 Layout lay, int *status) {
   using Sm = ScanSmem<D>;
-  constexpr int NT = D / 8, KK = D / 16, kParts = D / 64;
+  constexpr int NH = D / 16, KH = D / 32, kParts = D / kScanRows;  // 8-column blocks, k-steps of a half
   extern __shared__ __align__(128) uint8_t smem[];
   wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -358,38 +364,44 @@ gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *_
   const int G = ((eos - bos + C - 1) / C + L - 1) / L;
   const long long slot0 = bos / (C * L) + n;
   if (G < 2 || !in_range(status, slot0 + G, segment_slots(N, T, L) + 1)) return;
-  const int rl = 16 * warp + lane / 4, row = 64 * part + rl, col = 2 * (lane & 3);
+  const int rl = 16 * (warp & 1) + lane / 4;                      // rows rl, rl + 8 of the CTA's
+  const int mine = (warp >> 1) * (D / 2), his = D / 2 - mine;      // first columns of the two halves
+  const int col = 2 * (lane & 3);
   auto state_of = [&](size_t area, int g) {
-    return reinterpret_cast<float *>(ws + area) + ((size_t)(slot0 + g) * HV + h) * D * D;
+    return reinterpret_cast<float *>(ws + area) +
+           (((size_t)(slot0 + g) * HV + h) * D + kScanRows * part) * D;
   };
   auto fetch = [&](int g) {
     const uint32_t st = smem_addr(smem) + (g & 1) * Sm::kStage;
     cp_block(st, ws + lay.seg_m + ((size_t)(slot0 + g) * HV + h) * map_bytes(D), map_bytes(D));
-    const float *b = state_of(lay.seg_b, g) + 64 * part * D;
-    for (int i = threadIdx.x; i < 64 * D / 4; i += 128) {
+    const float *b = state_of(lay.seg_b, g);
+    for (int i = threadIdx.x; i < kScanRows * D / 4; i += 128) {
       const int r = i / (D / 4), p = i % (D / 4);
       cp16(st + Sm::kB + (r * Sm::kLd + 4 * p) * 4, b + r * D + 4 * p);
     }
   };
   if (G > 2) fetch(1);
   cp_commit();
-  float s[NT][4];
-  {
-    const float *p = state_of(lay.seg_b, 0) + (size_t)row * D + col;
+  float e[2][NH][4];  // this warp's half, the other warp's
+  auto load = [&](float(&x)[NH][4], const float *p, int ld) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < NH; ++i) {
       const float2 a = *reinterpret_cast<const float2 *>(p + 8 * i);
-      const float2 b = *reinterpret_cast<const float2 *>(p + 8 * D + 8 * i);
-      s[i][0] = a.x; s[i][1] = a.y; s[i][2] = b.x; s[i][3] = b.y;
+      const float2 b = *reinterpret_cast<const float2 *>(p + 8 * ld + 8 * i);
+      x[i][0] = a.x; x[i][1] = a.y; x[i][2] = b.x; x[i][3] = b.y;
     }
-  }
-  for (int g = 1;; ++g) {
-    float *p = state_of(lay.seg_e, g) + (size_t)row * D + col;
+  };
+  auto store = [&](float *p, int ld) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
-      *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
+    for (int i = 0; i < NH; ++i) {
+      *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(e[0][i][0], e[0][i][1]);
+      *reinterpret_cast<float2 *>(p + 8 * ld + 8 * i) = make_float2(e[0][i][2], e[0][i][3]);
     }
+  };
+  load(e[0], state_of(lay.seg_b, 0) + rl * D + mine + col, D);
+  load(e[1], state_of(lay.seg_b, 0) + rl * D + his + col, D);
+  for (int g = 1;; ++g) {
+    store(state_of(lay.seg_e, g) + rl * D + mine + col, D);
     if (g + 1 >= G) break;
     if (g + 2 < G) fetch(g + 1);
     cp_commit();
@@ -398,47 +410,53 @@ gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *_
     const uint8_t *st = smem + (g & 1) * Sm::kStage;
     const uint32_t mat = smem_addr(st);
     const float *scales = reinterpret_cast<const float *>(st + D * D * 4) + col;
+    float big0 = 0.f, big1 = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const float2 f = *reinterpret_cast<const float2 *>(scales + 8 * i);
-      s[i][0] *= f.x; s[i][1] *= f.y; s[i][2] *= f.x; s[i][3] *= f.y;
-    }
-    Scale a0, a1;
-    row_scales(s, a0, a1);
-    uint32_t hi[KK][4], lo[KK][4];
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
-    for (int kk = 0; kk < KK; ++kk) split_a(s, kk, a0, a1, hi[kk], lo[kk]);
-    const float *bp = reinterpret_cast<const float *>(st + Sm::kB) + rl * Sm::kLd + col;
-#pragma unroll
-    for (int j = 0; j < NT / 4; ++j) {
-      float acc[4][4];
-      zero(acc);
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-        for (int np = 0; np < 2; ++np) {
-          uint32_t b[4], bl[4];
-          load_rows_bt<D>(b, mat, 32 * j + 16 * np, 16 * kk, false);
-          load_rows_bt<D>(bl, mat, 32 * j + 16 * np, 16 * kk, true);
-          mma(acc[2 * np], hi[kk], b[0], b[1]);
-          mma(acc[2 * np + 1], hi[kk], b[2], b[3]);
-          mma(acc[2 * np], lo[kk], b[0], b[1]);
-          mma(acc[2 * np + 1], lo[kk], b[2], b[3]);
-          mma(acc[2 * np], hi[kk], bl[0], bl[1]);
-          mma(acc[2 * np + 1], hi[kk], bl[2], bl[3]);
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = *reinterpret_cast<const float2 *>(bp + 32 * j + 8 * i);
-        const float2 y = *reinterpret_cast<const float2 *>(bp + 8 * Sm::kLd + 32 * j + 8 * i);
-        float(&t)[4] = s[4 * j + i];
-        t[0] = fmaf(a0.s, acc[i][0], x.x);
-        t[1] = fmaf(a0.s, acc[i][1], x.y);
-        t[2] = fmaf(a1.s, acc[i][2], y.x);
-        t[3] = fmaf(a1.s, acc[i][3], y.y);
+      for (int i = 0; i < NH; ++i) {
+        float(&x)[4] = e[half][i];
+        const float2 f = *reinterpret_cast<const float2 *>(scales + (half ? his : mine) + 8 * i);
+        x[0] *= f.x; x[1] *= f.y; x[2] *= f.x; x[3] *= f.y;
+        big0 = fmaxf(big0, fmaxf(fabsf(x[0]), fabsf(x[1])));
+        big1 = fmaxf(big1, fmaxf(fabsf(x[2]), fabsf(x[3])));
       }
+    const Scale a0 = scale_of(quad_max(big0)), a1 = scale_of(quad_max(big1));
+    float acc[NH][4];
+    zero(acc);
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int kk = 0; kk < KH; ++kk) {
+        uint32_t hi[4], lo[4];
+        split_a(e[half], kk, a0, a1, hi, lo);
+        const int k0 = (half ? his : mine) + 16 * kk;
+#pragma unroll
+        for (int np = 0; np < NH / 2; ++np) {
+          uint32_t b[4], bl[4];
+          load_rows_bt<D>(b, mat, mine + 16 * np, k0, false);
+          load_rows_bt<D>(bl, mat, mine + 16 * np, k0, true);
+          mma(acc[2 * np], hi, b[0], b[1]);
+          mma(acc[2 * np + 1], hi, b[2], b[3]);
+          mma(acc[2 * np], lo, b[0], b[1]);
+          mma(acc[2 * np + 1], lo, b[2], b[3]);
+          mma(acc[2 * np], hi, bl[0], bl[1]);
+          mma(acc[2 * np + 1], hi, bl[2], bl[3]);
+        }
+      }
+    load(e[0], reinterpret_cast<const float *>(st + Sm::kB) + rl * Sm::kLd + mine + col, Sm::kLd);
+#pragma unroll
+    for (int i = 0; i < NH; ++i) {
+      float(&x)[4] = e[0][i];
+      x[0] = fmaf(a0.s, acc[i][0], x[0]);
+      x[1] = fmaf(a0.s, acc[i][1], x[1]);
+      x[2] = fmaf(a1.s, acc[i][2], x[2]);
+      x[3] = fmaf(a1.s, acc[i][3], x[3]);
     }
-    __syncthreads();  // the matrix has been read: the next fetch may take its place
+    float *all = reinterpret_cast<float *>(smem + Sm::kE) + rl * Sm::kLd + col;
+    store(all + mine, Sm::kLd);
+    __syncthreads();  // also: the matrix has been read, the next fetch may take its place
+    load(e[1], all + his, Sm::kLd);
   }
   cp_wait<0>();
 }
@@ -483,7 +501,7 @@ cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float sc
     const int bytes = (int)ScanSmem<D>::kBytes;
     e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    e = launch_behind(scan, dim3((unsigned)(N * HV * (D / 64))), 128, bytes, s, cu, N, T, HV,
+    e = launch_behind(scan, dim3((unsigned)(N * HV * (D / kScanRows))), 128, bytes, s, cu, N, T, HV,
                       static_cast<uint8_t *>(ws), lay, status);
     if (e != cudaSuccess) return e;
   }

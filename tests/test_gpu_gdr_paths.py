@@ -29,6 +29,19 @@ def problem(lens, HK, HV, **kw):
     return p
 
 
+def is_cut(kda, p):
+    """A segment's M, B and first state add to the records' bytes, which grow with N alone else."""
+    size = [kda.kda_gdr_chunk_fwd_workspace_bytes(n, p.T, p.HK, p.HV, p.D, p.dtype)
+            for n in (p.N, 1000, 1001)]
+    return size[0] > size[1] - (1000 - p.N) * (size[2] - size[1])
+
+
+@pytest.mark.parametrize("lens,HK,HV,cut", [(MANY, 2, 4, False), (LONG, 1, 2, True), (LONG, 1, 1, True),
+                                            ([1400, 1400, 1200], 1, 1, True)])
+def test_the_cases_take_their_form(kda, lens, HK, HV, cut):
+    assert is_cut(kda, Problem(lens, HK, HV, 128)) == cut
+
+
 def workspace(kda, p, fill=255):
     n = kda.kda_gdr_chunk_fwd_workspace_bytes(p.N, p.T, p.HK, p.HV, p.D, p.dtype)
     return torch.full((n,), fill, dtype=torch.uint8, device=DEV)
@@ -158,9 +171,9 @@ def test_backward_of_a_long_sequence(kda):
     check_backward(p, p.backward(kda))
 
 
-@pytest.mark.parametrize("cu", [[0, 1900, 40, 2000], [-5, 20, 1600, 2000], [0, 20, 1600, 1 << 30]])
+@pytest.mark.parametrize("cu", [[0, 3900, 40, 4000], [-5, 20, 3600, 4000], [0, 20, 3600, 1 << 30]])
 def test_malformed_cu_seqlens_are_reported_by_segments(kda, cu):
-    p = problem([700, 700, 600], 1, 1, dtype=BF16, seed=14)
+    p = problem([1400, 1400, 1200], 1, 1, dtype=BF16, seed=14)
     assert kda.kda_get_device_status() == 0
     p.cu = torch.tensor(cu, dtype=torch.int32, device=DEV)
     p.forward(kda.kda_gdr_chunk_fwd)
