@@ -30,6 +30,10 @@ namespace {
 using namespace gdr;
 
 // ---- reverse state pass ------------------------------------------------------------------
+// It reads the prep pass's records alone, so it is launched behind the forward's start (whose CTAs
+// wait for the prep pass before they let it go) and runs beside it on the SMs that are free; only its
+// end waits for the forward's, on which the local pass counts.  One after the other / beside one
+// another: 4096 tokens and 8 heads 750 / 523 us, ragged sequences of 1875 tokens and 8 heads 240 / 183.
 
 template <int D, int NW> struct ReverseSmem {
   static constexpr int kLd = 16 * NW + 4;  // row stride of the dO tile: no bank conflicts
@@ -57,7 +61,10 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
   seq_bounds(cu, n, T, status, bos, eos);
   const int chunks = (eos - bos + C - 1) / C;
   const long long slot0 = first_slot(bos, n);
-  if (!in_range(status, slot0 + chunks, slots(N, T) + 1)) return;
+  if (!in_range(status, slot0 + chunks, slots(N, T) + 1)) {
+    wait_for_previous_kernel();
+    return;
+  }
   const int row = (part * NW + warp) * 16 + lane / 4;  // this lane's value channels: row, row + 8
   const int col = 2 * (lane & 3);
 
@@ -269,6 +276,7 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
       *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
     }
   }
+  wait_for_previous_kernel();  // this one's end is the forward's too
 }
 
 // ---- local pass --------------------------------------------------------------------------
@@ -814,16 +822,14 @@ cudaError_t launch_reverse(const int32_t *cu, float scale, int N, int T, int HK,
                            const float *d_o, const float *d_sN, void *dv, float *d_s0, int *status,
                            cudaStream_t s) {
   auto kern = gdr_reverse_kernel<Tin, D, NW>;
-  const int bytes = (int)ReverseSmem<D, NW>::kBytes;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
   const long long ctas = (long long)N * HV * (D / (16 * NW));
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
-  kern<<<(unsigned)ctas, NW * 32, bytes, s>>>(d_o, d_sN, cu, scale, N, T, HK, HV,
-                                              static_cast<uint8_t *>(ws),
-                                              layout(N, T, HK, HV, D, true), static_cast<Tin *>(dv),
-                                              d_s0, status);
-  return cudaGetLastError();
+  const int bytes = chain_smem((int)ReverseSmem<D, NW>::kBytes, ctas);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return launch_behind(kern, dim3((unsigned)ctas), NW * 32, bytes, s, d_o, d_sN, cu, scale, N, T, HK, HV,
+                       static_cast<uint8_t *>(ws), layout(N, T, HK, HV, D, true), static_cast<Tin *>(dv),
+                       d_s0, status);
 }
 
 template <typename Tin, int D>

@@ -26,11 +26,14 @@ namespace kda {
 namespace {
 using namespace gdr;
 
-template <int D, int NW> struct StateSmem {
-  static constexpr uint32_t kK = 0, kQ = kQRows;
-  static constexpr uint32_t kScales = kq_tile_bytes(D);
-  static constexpr uint32_t kTp = kq_bytes(D);
-  static constexpr uint32_t kV = kTp + kTpBytes;               // [64][16 NW] 16-bit, swizzled
+// A stage: K (and Q), T (and P), the chunk's vectors, V.  The backward's forward needs no Q and no P.
+template <int D, int NW, int kRole> struct StateSmem {
+  static constexpr bool kAll = kRole != kKeep;
+  static constexpr int kRows = kAll ? kKq : C;                 // rows of the K (and Q) tile
+  static constexpr uint32_t kScales = (uint32_t)kRows * D * 2;
+  static constexpr uint32_t kTp = kScales + 128;               // T hi, lo (P hi, lo)
+  static constexpr uint32_t kVecs = kTp + (kAll ? 4 : 2) * kTriBytes;
+  static constexpr uint32_t kV = kVecs + gdr::kVecs * C * 4;   // [64][16 NW] 16-bit, swizzled
   static constexpr uint32_t kStage = kV + C * 32 * NW;
   static constexpr uint32_t kBytes = 2 * kStage;
 };
@@ -64,11 +67,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
 gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__restrict__ cu,
                  float scale, int N, int T, int HK, int HV, uint8_t *__restrict__ ws, Layout lay,
                  float *__restrict__ o, float *sN, int *status) {
-  using Sm = StateSmem<D, NW>;
+  using Sm = StateSmem<D, NW, kRole>;
   constexpr int NT = D / 8, KK = D / 16;
   constexpr int kParts = D / (16 * NW);  // CTAs per head
   extern __shared__ __align__(128) uint8_t smem[];
   wait_for_previous_kernel();  // before any way out: what comes next takes this one's end for the last one's
+  if (kRole == kKeep) next_kernel_may_start();  // the reverse pass only needs what is there by now
   const uint32_t sbase = smem_addr(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int b = blockIdx.x;
@@ -85,8 +89,18 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   auto load = [&](int c) {
     const uint32_t st = sbase + (c & 1) * Sm::kStage;
     const long long slot = slot0 + c;
-    cp_block(st, ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D), kq_bytes(D));
-    cp_block(st + Sm::kTp, ws + lay.tp + (size_t)(slot * HV + h) * kTpBytes, kTpBytes);
+    const uint8_t *kq = ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D);
+    const uint8_t *tp = ws + lay.tp + (size_t)(slot * HV + h) * kTpBytes;
+    if constexpr (Sm::kAll) {
+      cp_block(st, kq, kq_bytes(D));
+      cp_block(st + Sm::kTp, tp, kTpBytes);
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) cp_block(st + i * kQRows, kq + i * 2 * kQRows, kQRows);
+      cp_block(st + Sm::kScales, kq + kq_tile_bytes(D), 16);
+      cp_block(st + Sm::kTp, tp + kT_HI, 2 * kTriBytes);
+      cp_block(st + Sm::kVecs, tp + kVec, gdr::kVecs * C * 4);
+    }
     constexpr int kPieces = 2 * NW;
     const int t0 = bos + c * C, len = min(C, eos - t0);
     for (int i = threadIdx.x; i < C * kPieces; i += NW * 32) {
@@ -133,7 +147,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
     const uint32_t st = sbase + (c & 1) * Sm::kStage;
     const uint8_t *stp = smem + (c & 1) * Sm::kStage;
     const float2 kqs = *reinterpret_cast<const float2 *>(stp + Sm::kScales);
-    const float *vec = reinterpret_cast<const float *>(stp + Sm::kTp + kVec);
+    const float *vec = reinterpret_cast<const float *>(stp + Sm::kVecs);
     const int t0 = bos + c * C, len = min(C, eos - t0);
 
     if constexpr (kRole == kKeep) {
@@ -157,13 +171,13 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
 #pragma unroll
       for (int np = 0; np < 4; ++np) {
         uint32_t b[4];
-        load_b<kKq>(b, st + Sm::kK, 16 * np, 16 * kk);
+        load_b<Sm::kRows>(b, st, 16 * np, 16 * kk);
         mma(ks[2 * np], hi, b[0], b[1]);
         mma(ks[2 * np + 1], hi, b[2], b[3]);
         mma(ks[2 * np], lo, b[0], b[1]);
         mma(ks[2 * np + 1], lo, b[2], b[3]);
         if constexpr (kRole == kOut) {
-          load_b<kKq>(b, st + Sm::kQ, 16 * np, 16 * kk);
+          load_b<kKq>(b, st + kQRows, 16 * np, 16 * kk);
           mma(qs[2 * np], hi, b[0], b[1]);
           mma(qs[2 * np + 1], hi, b[2], b[3]);
           mma(qs[2 * np], lo, b[0], b[1]);
@@ -297,7 +311,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
 #pragma unroll
         for (int np = 0; np < 2; ++np) {
           uint32_t b[4];
-          load_bt<kKq>(b, st + Sm::kK, 32 * j + 16 * np, 16 * kk);
+          load_bt<Sm::kRows>(b, st, 32 * j + 16 * np, 16 * kk);
           mma(acc[2 * np], hi[kk], b[0], b[1]);
           mma(acc[2 * np + 1], hi[kk], b[2], b[3]);
           mma(acc[2 * np], lo[kk], b[0], b[1]);
@@ -315,7 +329,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
     __syncthreads();  // the other buffer is free for the chunk after next
   }
   cp_wait<0>();
-  next_kernel_may_start();
+  if (kRole != kKeep) next_kernel_may_start();
 
   if (kRole == kMap && pt.kind == 1) {
     uint8_t *m = ws + lay.seg_m + pt.seg * map_bytes(D);
@@ -466,12 +480,12 @@ cudaError_t launch_role(const void *v, const float *s0, const int32_t *cu, float
                         int HK, int HV, void *ws, const Layout &lay, float *o, float *sN, int *status,
                         cudaStream_t s) {
   auto kern = gdr_state_kernel<Tin, D, NW, kRole>;
-  const int bytes = (int)StateSmem<D, NW>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
   const long long units = kRole != kKeep && lay.seg_chunks ? segment_slots(N, T, lay.seg_chunks) : N;
   const long long ctas = units * HV * (D / (16 * NW)) * (kRole == kMap ? 2 : 1);
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
+  const int bytes = chain_smem((int)StateSmem<D, NW, kRole>::kBytes, ctas);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
   return launch_behind(kern, dim3((unsigned)ctas), NW * 32, bytes, s, static_cast<const Tin *>(v), s0,
                        cu, scale, N, T, HK, HV, static_cast<uint8_t *>(ws), lay, o, sN, status);
 }

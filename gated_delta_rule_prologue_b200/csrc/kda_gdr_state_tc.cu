@@ -163,6 +163,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
                     int *status) {
   extern __shared__ uint8_t smem_raw[];
   wait_for_previous_kernel();
+  if (kRole == kKeep) next_kernel_may_start();  // the reverse pass only needs what is there by now
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   Small &sm = *reinterpret_cast<Small *>(smem + 2 * kStage);
