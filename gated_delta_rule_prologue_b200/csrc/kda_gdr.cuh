@@ -189,6 +189,31 @@ __device__ __forceinline__ bool chunk_of_slot(const int32_t *cu, int N, int T, l
   return true;
 }
 
+// Sequence of a chain by its place in the launch, the longest first (equal lengths by index): for
+// launches whose chains do not all run at once, so that no long chain starts when the others end, and
+// of up to kRanked sequences.  Ten packed prompts of 512 to 16384 tokens, 32 heads: 2255 -> 2165 us; 0.5 us
+// more per CTA.  By all threads of a block; not inlined, for the callers' registers.
+constexpr int kRanked = 64;
+[[maybe_unused]] static __device__ __noinline__ int sequence_of_place(const int32_t *cu, int N, int T,
+                                                                      int place, int *status) {
+  __shared__ int length[kRanked], found;
+  const int i = threadIdx.x;
+  int mine = 0;
+  if (i < N) {
+    int bos, eos;
+    seq_bounds(cu, i, T, status, bos, eos);
+    length[i] = mine = eos - bos;
+  }
+  __syncthreads();
+  if (i < N) {
+    int before = 0;
+    for (int j = 0; j < N; ++j) before += length[j] > mine || (length[j] == mine && j < i);
+    if (before == place) found = i;
+  }
+  __syncthreads();
+  return found;
+}
+
 // What a launch of the state pass is for.
 enum Role {
   kOut,   // the read-out and the last states; of segments from the scan's states, if sequences are cut
@@ -203,7 +228,7 @@ struct Part {
   long long slot;      // of the first chunk
 };
 // Part b (segments, or whole sequences, times heads; times two for maps); false: nothing to do.
-template <int kRole>
+template <int kRole, bool kRanks>
 __device__ __forceinline__ bool part_of(int b, const int32_t *cu, int N, int T, int HV, const Layout &lay,
                                         int *status, Part &p) {
   p.kind = kRole == kMap ? b & 1 : 0;
@@ -214,6 +239,7 @@ __device__ __forceinline__ bool part_of(int b, const int32_t *cu, int N, int T, 
   p.seg = 0;
   const int L = kRole == kKeep ? 0 : lay.seg_chunks;
   if (L == 0) {
+    if (kRanks && gridDim.x > 148 && cu && N <= kRanked) p.n = sequence_of_place(cu, N, T, p.n, status);
     seq_bounds(cu, p.n, T, status, p.bos, p.eos);
     p.end = (p.eos - p.bos + C - 1) / C;
   } else {

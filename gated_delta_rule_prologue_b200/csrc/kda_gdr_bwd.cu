@@ -55,8 +55,10 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = smem_addr(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = blockIdx.x % kParts, nh = blockIdx.x / kParts;
-  const int n = nh / HV, h = nh % HV, hk = h / (HV / HK);
+  const int part = blockIdx.x % kParts, h = blockIdx.x / kParts % HV, hk = h / (HV / HK);
+  int n = blockIdx.x / kParts / HV;
+  if (NW == 8 && gridDim.x > 148 && cu && N <= kRanked) n = sequence_of_place(cu, N, T, n, status);
+  const size_t nh = (size_t)n * HV + h;
   int bos, eos;
   seq_bounds(cu, n, T, status, bos, eos);
   const int chunks = (eos - bos + C - 1) / C;

@@ -79,7 +79,7 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
   const int part = b % kParts;
   b /= kParts;
   Part pt;
-  if (!part_of<kRole>(b, cu, N, T, HV, lay, status, pt)) return;
+  if (!part_of<kRole, D == 64>(b, cu, N, T, HV, lay, status, pt)) return;
   const int h = pt.h, hk = h / (HV / HK), bos = pt.bos, eos = pt.eos, first = pt.first, end = pt.end;
   const long long slot0 = pt.slot - first;
   const int ch0 = (part * NW + warp) * 16;     // the warp's first value channel

@@ -169,7 +169,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
   Small &sm = *reinterpret_cast<Small *>(smem + 2 * kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   Part pt;
-  if (!part_of<kRole>(blockIdx.x, cu, N, T, HV, lay, status, pt)) return;
+  if (!part_of<kRole, true>(blockIdx.x, cu, N, T, HV, lay, status, pt)) return;
   const int h = pt.h, hk = h / (HV / HK);
   const int bos = pt.bos + pt.first * C, eos = pt.eos, chunks = pt.end - pt.first;  // of this part
   const long long slot0 = pt.slot;

@@ -165,6 +165,15 @@ def test_backward_outside_every_sequence(kda, state):
     check_backward(p, p.backward(kda))
 
 
+def test_more_sequences_than_are_ranked(kda):
+    """Up to 64 sequences start longest first, more as they come."""
+    for lens in ([3, 70, 1, 0, 65] * 14, [3, 70, 1, 0, 65] * 12 + [64] * 4):
+        p = Problem(lens, 1, 2, 128, BF16, seed=16)
+        p.forward(kda.kda_gdr_chunk_fwd)
+        check_forward(p, CHUNK)
+        check_backward(p, p.backward(kda))
+
+
 def test_backward_of_a_long_sequence(kda):
     p = Problem([1500], 1, 1, 128, BF16, seed=13)
     p.g *= 0.3
