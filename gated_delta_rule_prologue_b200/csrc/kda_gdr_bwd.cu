@@ -22,6 +22,10 @@
 // Per value head and chunk at D = 128 the reverse pass is 504 MMAs per warp (8 warps), the local
 // pass about 1000; a chunk of the local pass reads 270 KB.  The local pass keeps S and dS' as split
 // fp16 rows in shared memory (128 KB) with K, Q, U and dO or X, one persistent CTA per SM.
+// Bounds: the reverse pass a chain's latency, 6.9 us a chunk (64 chains of 32 chunks, 16 value channels
+// per warp on 128 SMs: 220 us); the local pass the latency of its steps with two warps per SM quarter
+// (the tensor pipe is busy 34% of the time, 28% of the issue slots), 26 us a chunk and SM: 2048 chunks
+// 372 us, 629 MB.  16 warps per CTA: 428.
 #include "kda_gdr.cuh"
 #include "kda_tcgen05.cuh"
 

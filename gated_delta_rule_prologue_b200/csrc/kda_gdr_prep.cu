@@ -12,8 +12,11 @@
 // A and D are B operands read along their rows from shared memory.  Block substitution adds
 // nothing to the error of the element-wise one, and nothing is divided.
 //
-// Bound: the latency of one item's steps; four CTAs per SM (128 registers, 44 KB) hide one
-// another's.  Bytes per item: 2 x 64 x D in, 33 KB out, and the KQ record once per key head.
+// Bound: the latency of one item's steps; four CTAs per SM (128 registers, 47 KB) hide one
+// another's: 41% of the issue slots, 53% of the shared-memory wavefronts, and no one stall reason
+// above a fifth.  Bytes per item: 2 x 64 x D x 2 in, 33 KB out, and the KQ record once per key head.
+// D = 128, 29 920 items, two value heads per key head: 811 us, 1.79 GB, 2.2 TB/s.  Three, five or six
+// CTAs per SM: 6, 0 and 10% longer.
 #include <type_traits>
 
 #include "kda_gdr.cuh"

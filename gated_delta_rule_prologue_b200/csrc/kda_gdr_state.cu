@@ -14,10 +14,13 @@
 // The records and the V tile of the next chunk arrive by cp.async while this one is computed;
 // the CTA's two barriers per chunk only guard the two buffers.
 //
-// D = 128: 504 MMAs (16 x 8 x 16) per warp and chunk.  mma.sync runs at 9 cycles per MMA and SM
-// quarter (527 TFLOP/s measured over the GPU); with eight warps (a whole head) per CTA that is
-// what bounds the pass when there are chains enough, and with fewer chains than SMs a chain's
-// latency does.  Then a head is split over two CTAs of four warps, one per SM quarter.
+// D = 128: 504 MMAs (16 x 8 x 16) per warp and chunk, one warp per SM quarter, 64 value channels per
+// CTA.  mma.sync runs at 9 cycles per MMA and SM quarter (527 TFLOP/s measured over the GPU), 2.4 us a
+// chunk; bound by the chain's latency, 4.9 us a chunk with the read-out and 3.9 without (64 chains of
+// 32 chunks, split over 128 SMs: 125 us).  A whole head on eight warps of one CTA took 7.7.
+//
+// For more heads than that, and for segments, D = 128 runs on tcgen05 (kda_gdr_state_tc.cu), which
+// takes the same time for a whole head on one SM.
 #include <type_traits>
 
 #include "kda_gdr.cuh"
@@ -361,7 +364,8 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
 // E^T is the A operand of its own next step, as S^T in the pass above.  Four warps: 16 value channels
 // times half the key channels of the result each, and the halves are exchanged after every step.  M
 // comes split, row by row; its rows' scales go to E's columns.
-// Bound: a step's chain; 192 MMAs a warp.
+// Bound: a step's chain, 192 MMAs a warp, about 2 us at D = 128 (64 value channels and whole rows per warp:
+// 3.2; all 128 channels with M split here: 6).
 template <int D>
 __global__ void __launch_bounds__(128, 1)
 gdr_scan_kernel(const int32_t *__restrict__ cu, int N, int T, int HV, uint8_t *__restrict__ ws,
@@ -496,8 +500,8 @@ cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float sc
                      cudaStream_t s) {
   const Layout lay = layout(N, T, HK, HV, D, bwd);
   // D = 128: two CTAs of four warps per head, one per SM, if they all run at once, or else, and for
-  // segments, which fill the SMs by themselves, the tcgen05 form with one CTA per head.  A chunk takes
-  // 4.9 us in either with the read-out; without it 4.1 us here and 4.4 (maps) and 5.3 us (kept) there.
+  // segments, which fill the SMs by themselves, the tcgen05 form with one CTA per head.  Microseconds a
+  // chunk, here and there: with the read-out 4.9 and 5.3, kept for the backward 3.9 and 5.3, maps 4.1 and 4.2.
   const bool tensor_memory = D == 128 && (lay.seg_chunks || (long long)N * HV * 2 > 148);
   const kda_dtype dt = std::is_same<Tin, __half>::value ? KDA_F16 : KDA_BF16;
   if (bwd)

@@ -23,7 +23,10 @@
 // MMA is 64 - 16 k columns wide.
 //
 // Bound: the latency of a chunk's chain (three MMA groups, each followed by a TMEM read, a split
-// and a TMEM write); one CTA per SM (all 512 TMEM columns).
+// and a TMEM write), 5.3 us with the read-out, of which the MMAs are about 2; one CTA per SM (all 512
+// TMEM columns).  Ten prompts, 59566 tokens, 32 heads: 1.39 ms, the chain of the longest (256 chunks);
+// the chunks of all would take 1.0 ms on 148 SMs.  Four warps instead of eight on the chain: 514 us
+// where eight take 342.
 #include <type_traits>
 
 #include "kda_gdr.cuh"
