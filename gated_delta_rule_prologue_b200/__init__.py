@@ -797,7 +797,8 @@ def kda_gdr_chunk_bwd(q, k, v, g, beta, d_o, *, scale: float = 1.0, initial_stat
                       workspace="auto", stream=None):
     """Gradients of :func:`kda_gdr_chunk_fwd` for L = sum(d_o * o) + sum(d_final_state *
     final_state).  Returns ``(dq, dk, dv, dg, dbeta, d_initial_state)``: the first three of q's
-    dtype, the others fp32, the last None unless wanted; outputs not given are allocated."""
+    dtype, the others fp32, the last None unless wanted; outputs not given are allocated.  Rows of
+    tokens outside every sequence are left as they are (undefined where allocated here)."""
     N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
     dev, f32, sq, dt = _cuda_device(q), torch.float32, (N, HV, D, D), _dtype(q)
     heads, qk, vo, act = (T, HV), (T, HK, D), (T, HV, D), q.dtype
