@@ -80,8 +80,11 @@ def test_workspace_sizes(kda):
         for a in ((1, 100, 2, 4, 128, 0), (1, 100, 2, 4, 32, 1), (1, 0, 2, 4, 128, 1),
                   (0, 100, 2, 4, 128, 1), (1, 100, 3, 4, 128, 1), (1, 100, 2, 4, 128, 9)):
             assert fn(*a) == 0, a
-    # every sequence adds at most its own ragged chunk
-    assert f(9, 1000, 2, 4, 128, 1) > f(1, 1000, 2, 4, 128, 1)
+    # every sequence adds its own ragged chunk (the forward's one long sequence is cut, with segments'
+    # maps and states in its workspace, so it is compared where nothing is cut)
+    assert b(9, 1000, 2, 4, 128, 1) > b(1, 1000, 2, 4, 128, 1)
+    assert f(9, 100, 2, 4, 128, 1) > f(1, 100, 2, 4, 128, 1)
+    assert f(1, 1000, 2, 4, 128, 1) > f(9, 1000, 2, 4, 128, 1)
     assert b(1, 1000, 2, 4, 128, 1) > f(1, 1000, 2, 4, 128, 1)
     # sizes whose records pass 32 bits
     assert f(1, 1 << 20, 64, 64, 128, 1) > 1 << 32
