@@ -19,11 +19,11 @@
 // (each decay factor's gradient times the factor itself, so nothing is divided by a decay).
 // dQ and dK of a key head's value heads are summed in registers in a fixed order.
 //
-// Per value head and chunk at D = 128 the reverse pass is 504 MMAs per warp (8 warps), the local
-// pass about 1000; a chunk of the local pass reads 270 KB.  The local pass keeps S and dS' as split
+// Per value head and chunk at D = 128 the reverse pass is 504 MMAs per 16 value channels, the local
+// pass about 1000 per warp (8 warps); a chunk of the local pass reads 270 KB.  The local pass keeps S and dS' as split
 // fp16 rows in shared memory (128 KB) with K, Q, U and dO or X, one persistent CTA per SM.
-// Bounds: the reverse pass a chain's latency, 6.9 us a chunk (64 chains of 32 chunks, 16 value channels
-// per warp on 128 SMs: 220 us); the local pass the latency of its steps with two warps per SM quarter
+// Bounds: the reverse pass a chain's latency, 5.8 us a chunk (64 chains of 32 chunks on 128 SMs: 186 us);
+// the local pass the latency of its steps with two warps per SM quarter
 // (the tensor pipe is busy 34% of the time, 28% of the issue slots), 26 us a chunk and SM: 2048 chunks
 // 372 us, 629 MB.  16 warps per CTA: 428.
 #include "kda_gdr.cuh"
@@ -39,7 +39,9 @@ using namespace gdr;
 // end waits for the forward's, on which the local pass counts.  One after the other / beside one
 // another: 4096 tokens and 8 heads 750 / 523 us, ragged sequences of 1875 tokens and 8 heads 240 / 183.
 
-template <int D, int NW> struct ReverseSmem {
+// The form of whole heads: eight warps per CTA, 16 value channels each.
+template <int D> struct ReverseSmem {
+  static constexpr int NW = D / 16;
   static constexpr int kLd = 16 * NW + 4;  // row stride of the dO tile: no bank conflicts
   static constexpr uint32_t kK = 0, kQ = kQRows;
   static constexpr uint32_t kScales = kq_tile_bytes(D);
@@ -49,19 +51,19 @@ template <int D, int NW> struct ReverseSmem {
   static constexpr uint32_t kBytes = 2 * kStage;
 };
 
-template <typename Tin, int D, int NW>
-__global__ void __launch_bounds__(NW * 32, 1)
+template <typename Tin, int D>
+__global__ void __launch_bounds__(2 * D, 1)
 gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32_t *__restrict__ cu,
                    float scale, int N, int T, int HK, int HV, uint8_t *__restrict__ ws, Layout lay,
                    Tin *__restrict__ dv, float *d_s0, int *status) {
-  using Sm = ReverseSmem<D, NW>;
-  constexpr int NT = D / 8, KK = D / 16, kParts = D / (16 * NW);
+  using Sm = ReverseSmem<D>;
+  constexpr int NW = Sm::NW, NT = D / 8, KK = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sbase = smem_addr(smem);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int part = blockIdx.x % kParts, h = blockIdx.x / kParts % HV, hk = h / (HV / HK);
-  int n = blockIdx.x / kParts / HV;
-  if (NW == 8 && gridDim.x > 148 && cu && N <= kRanked) n = sequence_of_place(cu, N, T, n, status);
+  const int h = blockIdx.x % HV, hk = h / (HV / HK);
+  int n = blockIdx.x / HV;
+  if (gridDim.x > 148 && cu && N <= kRanked) n = sequence_of_place(cu, N, T, n, status);
   const size_t nh = (size_t)n * HV + h;
   int bos, eos;
   seq_bounds(cu, n, T, status, bos, eos);
@@ -71,7 +73,7 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
     wait_for_previous_kernel();
     return;
   }
-  const int row = (part * NW + warp) * 16 + lane / 4;  // this lane's value channels: row, row + 8
+  const int row = warp * 16 + lane / 4;  // this lane's value channels: row, row + 8
   const int col = 2 * (lane & 3);
 
   auto load = [&](int c) {
@@ -84,7 +86,7 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
     for (int i = threadIdx.x; i < C * kPieces; i += NW * 32) {
       const int r = i / kPieces, p = i % kPieces;
       cp16(st + Sm::kDo + (r * Sm::kLd + 4 * p) * 4,
-           d_o + ((size_t)(t0 + min(r, len - 1)) * HV + h) * D + part * NW * 16 + 4 * p, r < len);
+           d_o + ((size_t)(t0 + min(r, len - 1)) * HV + h) * D + 4 * p, r < len);
     }
   };
   if (chunks > 0) load(chunks - 1);
@@ -93,7 +95,7 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
   float s[NT][4];  // dS^T
   zero(s);
   if (d_sN) {
-    const float *p = d_sN + ((size_t)nh * D + row) * D + col;
+    const float *p = d_sN + (nh * D + row) * D + col;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const float2 a = *reinterpret_cast<const float2 *>(p + 8 * i);
@@ -275,7 +277,7 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
   }
   cp_wait<0>();
   if (d_s0) {
-    float *p = d_s0 + ((size_t)nh * D + row) * D + col;
+    float *p = d_s0 + (nh * D + row) * D + col;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
@@ -283,6 +285,303 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
     }
   }
   wait_for_previous_kernel();  // this one's end is the forward's too
+}
+
+// The form of 64 value channels per CTA: warps 0-3 carry the chain, and warps 4-7 compute, one chunk ahead
+// of them, what does not depend on dS': (P^T dO~)^T and ((G dO~)^T Q).  A lane of warp w + 4 holds the
+// elements that the same lane of warp w adds, so they pass through shared memory lane by lane.  The
+// chain is 316 of the 504 MMAs: 5.8 us a chunk, 6.9 with all of them on four warps (4 x 2048 tokens, 16
+// heads: 749 -> 716 us).
+template <int D> struct PairSmem {
+  static constexpr int kLd = 64 + 4;                            // row stride of the dO tile
+  static constexpr uint32_t kTile = (uint32_t)C * D * 2;         // K or Q
+  static constexpr uint32_t kTri = 2 * kTriBytes;                // T or P, hi and lo
+  static constexpr uint32_t kVecBytes = gdr::kVecs * C * 4;
+  // the chain's stages: K, scales, T, vectors; the others': Q, scales, P, vectors, dO
+  static constexpr uint32_t kScales = kTile, kTp = kScales + 128, kVecs = kTp + kTri, kDo = kVecs + kVecBytes;
+  static constexpr uint32_t kChain = kDo, kSide = kDo + C * kLd * 4;
+  static constexpr uint32_t kSides = 2 * kChain;
+  static constexpr uint32_t kGiven = kSides + 2 * kSide;         // [4 warps][8 + D / 8][32] float4
+  static constexpr uint32_t kBytes = kGiven + 4 * (8 + D / 8) * 32 * 16;
+};
+
+__device__ __forceinline__ void half_barrier(int half) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+}
+
+template <typename Tin, int D>
+__global__ void __launch_bounds__(256, 1)
+gdr_reverse_pair_kernel(const float *__restrict__ d_o, const float *d_sN, const int32_t *__restrict__ cu,
+                        float scale, int N, int T, int HK, int HV, uint8_t *__restrict__ ws, Layout lay,
+                        Tin *__restrict__ dv, float *d_s0, int *status) {
+  using Sm = PairSmem<D>;
+  constexpr int NT = D / 8, KK = D / 16, kParts = D / 64;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5, half = threadIdx.x >> 7;
+  const int part = blockIdx.x % kParts, nh = blockIdx.x / kParts;
+  const int n = nh / HV, h = nh % HV, hk = h / (HV / HK);
+  int bos, eos;
+  seq_bounds(cu, n, T, status, bos, eos);
+  const int chunks = (eos - bos + C - 1) / C;
+  const long long slot0 = first_slot(bos, n);
+  if (!in_range(status, slot0 + chunks, slots(N, T) + 1)) {
+    wait_for_previous_kernel();
+    return;
+  }
+  const int row = (part * 4 + warp) * 16 + lane / 4;  // this lane's value channels: row, row + 8
+  const int col = 2 * (lane & 3);
+  float4 *given = reinterpret_cast<float4 *>(smem + Sm::kGiven) + warp * (8 + NT) * 32 + lane;
+
+  auto copy = [&](uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    for (uint32_t i = tid * 16; i < bytes; i += 128 * 16) cp16(dst + i, src + i);
+  };
+  // Chunk c's stage of this half.
+  const uint32_t stages = sbase + (half ? Sm::kSides : 0), stage_bytes = half ? Sm::kSide : Sm::kChain;
+  auto load = [&](int c) {
+    const uint32_t st = stages + (c & 1) * stage_bytes;
+    const long long slot = slot0 + c;
+    const uint8_t *kq = ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D);
+    const uint8_t *tp = ws + lay.tp + (size_t)(slot * HV + h) * kTpBytes;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) copy(st + i * kQRows, kq + (2 * i + half) * kQRows, kQRows);
+    copy(st + Sm::kScales, kq + kq_tile_bytes(D), 16);
+    copy(st + Sm::kTp, tp + (half ? kP_HI : kT_HI), Sm::kTri);
+    copy(st + Sm::kVecs, tp + kVec, Sm::kVecBytes);
+    if (half == 0) return;
+    const int t0 = bos + c * C, len = min(C, eos - t0);
+    for (int i = tid; i < C * 16; i += 128) {
+      const int r = i / 16, p = i % 16;
+      cp16(st + Sm::kDo + (r * Sm::kLd + 4 * p) * 4,
+           d_o + ((size_t)(t0 + min(r, len - 1)) * HV + h) * D + part * 64 + 4 * p, r < len);
+    }
+  };
+  if (chunks > 0) load(chunks - 1);
+  cp_commit();
+
+  // Lower triangular products (X^T lower)^T: the tile's rows are the sum's index.
+  auto triangular = [&](float (&out)[8][4], const float (&x)[8][4], uint32_t tile, Scale &r0, Scale &r1) {
+    zero(out);
+    row_scales(x, r0, r1);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      uint32_t hi[4], lo[4];
+      split_a(x, kk, r0, r1, hi, lo);
+#pragma unroll
+      for (int np = 0; np <= kk; ++np) {
+        uint32_t b[4], bl[4];
+        load_bt(b, tile, 16 * np, 16 * kk);
+        load_bt(bl, tile + kTriBytes, 16 * np, 16 * kk);
+        mma(out[2 * np], hi, b[0], b[1]);
+        mma(out[2 * np + 1], hi, b[2], b[3]);
+        mma(out[2 * np], lo, b[0], b[1]);
+        mma(out[2 * np + 1], lo, b[2], b[3]);
+        mma(out[2 * np], hi, bl[0], bl[1]);
+        mma(out[2 * np + 1], hi, bl[2], bl[3]);
+      }
+    }
+  };
+
+  if (half) {
+    for (int c = chunks - 1; c >= -1; --c) {
+      float pd[8][4], qd[NT][4];
+      if (c >= 0) {
+        if (c > 0) load(c - 1);
+        cp_commit();
+        cp_wait<1>();
+        half_barrier(1);
+        const uint32_t st = stages + (c & 1) * stage_bytes;
+        const uint8_t *stp = smem + (st - sbase);
+        const float qs = *reinterpret_cast<const float *>(stp + Sm::kScales + 4);
+        const float *vec = reinterpret_cast<const float *>(stp + Sm::kVecs);
+        const float *dop = reinterpret_cast<const float *>(stp + Sm::kDo) + warp * 16 + lane / 4;
+        // dO~^T of the warp's channels, and (P^T dO~)^T: P's scales go to the other operand.
+        float x[8][4], t[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 p = *reinterpret_cast<const float2 *>(vec + kVecP * C + 8 * i + col);
+          const float2 g = *reinterpret_cast<const float2 *>(vec + kVecG * C + 8 * i + col);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float d = scale * dop[(8 * i + col + (e & 1)) * Sm::kLd + 8 * (e >> 1)];
+            t[i][e] = (e & 1 ? p.y : p.x) * d;
+            x[i][e] = (e & 1 ? g.y : g.x) * d;  // G dO~
+          }
+        }
+        Scale r0, r1;
+        triangular(pd, t, st + Sm::kTp, r0, r1);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          pd[i][0] *= r0.s; pd[i][1] *= r0.s; pd[i][2] *= r1.s; pd[i][3] *= r1.s;
+        }
+        row_scales(x, r0, r1);
+        uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) split_a(x, kk, r0, r1, hi[kk], lo[kk]);
+        const float w0 = r0.s * qs, w1 = r1.s * qs;
+        zero(qd);
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            uint32_t b[4];
+            load_bt(b, st, 16 * j, 16 * kk);
+            mma(qd[2 * j], hi[kk], b[0], b[1]);
+            mma(qd[2 * j + 1], hi[kk], b[2], b[3]);
+            mma(qd[2 * j], lo[kk], b[0], b[1]);
+            mma(qd[2 * j + 1], lo[kk], b[2], b[3]);
+          }
+#pragma unroll
+          for (int i = 2 * j; i < 2 * j + 2; ++i) {
+            qd[i][0] *= w0; qd[i][1] *= w0; qd[i][2] *= w1; qd[i][3] *= w1;
+          }
+        }
+      }
+      __syncthreads();  // the chain has taken what was given for the chunk before
+      if (c >= 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) given[i * 32] = make_float4(pd[i][0], pd[i][1], pd[i][2], pd[i][3]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          given[(8 + i) * 32] = make_float4(qd[i][0], qd[i][1], qd[i][2], qd[i][3]);
+      }
+      __syncthreads();
+    }
+    cp_wait<0>();
+    wait_for_previous_kernel();
+    return;
+  }
+
+  float s[NT][4];  // dS^T
+  zero(s);
+  if (d_sN) {
+    const float *p = d_sN + ((size_t)nh * D + row) * D + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const float2 a = *reinterpret_cast<const float2 *>(p + 8 * i);
+      const float2 b = *reinterpret_cast<const float2 *>(p + 8 * D + 8 * i);
+      s[i][0] = a.x; s[i][1] = a.y; s[i][2] = b.x; s[i][3] = b.y;
+    }
+  }
+  __syncthreads();
+  __syncthreads();
+  for (int c = chunks - 1; c >= 0; --c) {
+    if (c > 0) load(c - 1);
+    cp_commit();
+    cp_wait<1>();
+    half_barrier(0);
+    const uint32_t st = stages + (c & 1) * stage_bytes;
+    const uint8_t *stp = smem + (st - sbase);
+    const float ks = *reinterpret_cast<const float *>(stp + Sm::kScales);
+    const float *vec = reinterpret_cast<const float *>(stp + Sm::kVecs);
+    const int t0 = bos + c * C, len = min(C, eos - t0);
+    const size_t rec = (size_t)(slot0 + c) * HV + h;
+    {
+      float *p = reinterpret_cast<float *>(ws + lay.dstate) + rec * D * D + row;
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[(8 * i + col + (e & 1)) * D + 8 * (e >> 1)] = s[i][e];
+    }
+    // (K dS')^T.
+    float du[8][4];
+    zero(du);
+    Scale a0, a1, r0, r1;
+    row_scales(s, a0, a1);
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      uint32_t hi[4], lo[4];
+      split_a(s, kk, a0, a1, hi, lo);
+#pragma unroll
+      for (int np = 0; np < 4; ++np) {
+        uint32_t b[4];
+        load_b(b, st, 16 * np, 16 * kk);
+        mma(du[2 * np], hi, b[0], b[1]);
+        mma(du[2 * np + 1], hi, b[2], b[3]);
+        mma(du[2 * np], lo, b[0], b[1]);
+        mma(du[2 * np + 1], lo, b[2], b[3]);
+      }
+    }
+    // dU^T, its tokens scaled for T's rows.
+    {
+      const float f0 = a0.s * ks, f1 = a1.s * ks;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 e = *reinterpret_cast<const float2 *>(vec + kVecE * C + 8 * i + col);
+        const float2 tt = *reinterpret_cast<const float2 *>(vec + kVecT * C + 8 * i + col);
+        const float4 pd = given[i * 32];
+        du[i][0] = tt.x * (e.x * (f0 * du[i][0]) + pd.x);
+        du[i][1] = tt.y * (e.y * (f0 * du[i][1]) + pd.y);
+        du[i][2] = tt.x * (e.x * (f1 * du[i][2]) + pd.z);
+        du[i][3] = tt.y * (e.y * (f1 * du[i][3]) + pd.w);
+      }
+    }
+    // X^T = (T^T dU)^T.
+    float t[8][4];
+    triangular(t, du, st + Sm::kTp, r0, r1);
+    {
+      float *xp = reinterpret_cast<float *>(ws + lay.x) + rec * C * D + row;
+      Tin *vp = dv + ((size_t)t0 * HV + h) * D + row;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 bt = *reinterpret_cast<const float2 *>(vec + kVecBeta * C + 8 * i + col);
+        const float2 g = *reinterpret_cast<const float2 *>(vec + kVecG * C + 8 * i + col);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = 8 * i + col + (e & 1);
+          const float xx = (e >> 1 ? r1.s : r0.s) * t[i][e];
+          xp[tok * D + 8 * (e >> 1)] = xx;
+          const float dr = xx * (e & 1 ? bt.y : bt.x);
+          if (tok < len) vp[(size_t)tok * HV * D + 8 * (e >> 1)] = from_f32<Tin>(dr);
+          t[i][e] = (e & 1 ? g.y : g.x) * dr;  // G beta X
+        }
+      }
+    }
+    // dS^T = G_C dS'^T + (G dO~)^T Q - (G beta X)^T K.
+    row_scales(t, r0, r1);
+    uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) split_a(t, kk, r0, r1, hi[kk], lo[kk]);
+    const float gl = vec[kVecG * C + C - 1];
+    const float w0 = -r0.s * ks, w1 = -r1.s * ks;
+#pragma unroll
+    for (int j = 0; j < NT / 4; ++j) {
+      float acc[4][4];
+      zero(acc);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int np = 0; np < 2; ++np) {
+          uint32_t b[4];
+          load_bt(b, st, 32 * j + 16 * np, 16 * kk);
+          mma(acc[2 * np], hi[kk], b[0], b[1]);
+          mma(acc[2 * np + 1], hi[kk], b[2], b[3]);
+          mma(acc[2 * np], lo[kk], b[0], b[1]);
+          mma(acc[2 * np + 1], lo[kk], b[2], b[3]);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float(&y)[4] = s[4 * j + i];
+        const float4 qd = given[(8 + 4 * j + i) * 32];
+        y[0] = fmaf(gl, y[0], fmaf(w0, acc[i][0], qd.x));
+        y[1] = fmaf(gl, y[1], fmaf(w0, acc[i][1], qd.y));
+        y[2] = fmaf(gl, y[2], fmaf(w1, acc[i][2], qd.z));
+        y[3] = fmaf(gl, y[3], fmaf(w1, acc[i][3], qd.w));
+      }
+    }
+    __syncthreads();
+    __syncthreads();
+  }
+  cp_wait<0>();
+  if (d_s0) {
+    float *p = d_s0 + ((size_t)nh * D + row) * D + col;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      *reinterpret_cast<float2 *>(p + 8 * i) = make_float2(s[i][0], s[i][1]);
+      *reinterpret_cast<float2 *>(p + 8 * D + 8 * i) = make_float2(s[i][2], s[i][3]);
+    }
+  }
+  wait_for_previous_kernel();
 }
 
 // ---- local pass --------------------------------------------------------------------------
@@ -823,17 +1122,27 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
   }
 }
 
-template <typename Tin, int D, int NW>
+template <typename Tin, int D>
 cudaError_t launch_reverse(const int32_t *cu, float scale, int N, int T, int HK, int HV, void *ws,
                            const float *d_o, const float *d_sN, void *dv, float *d_s0, int *status,
                            cudaStream_t s) {
-  auto kern = gdr_reverse_kernel<Tin, D, NW>;
-  const long long ctas = (long long)N * HV * (D / (16 * NW));
+  // Two CTAs of 64 value channels per head as long as all of them run at once, else whole heads (8.2 us a
+  // chunk where two CTAs on the same SM in turn take 11.6), as the forward (kda_gdr_state.cu).
+  const bool whole = D == 128 && (long long)N * HV * 2 > 148;
+  void (*kern)(const float *, const float *, const int32_t *, float, int, int, int, int, uint8_t *, Layout,
+               Tin *, float *, int *) = gdr_reverse_pair_kernel<Tin, D>;
+  int bytes = (int)PairSmem<D>::kBytes;
+  long long ctas = (long long)N * HV * (D / 64);
+  if constexpr (D == 128)
+    if (whole) {
+      kern = gdr_reverse_kernel<Tin, D>;
+      bytes = (int)ReverseSmem<D>::kBytes;
+      ctas = (long long)N * HV;
+    }
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
-  const int bytes = chain_smem((int)ReverseSmem<D, NW>::kBytes, ctas);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  return launch_behind(kern, dim3((unsigned)ctas), NW * 32, bytes, s, d_o, d_sN, cu, scale, N, T, HK, HV,
+  return launch_behind(kern, dim3((unsigned)ctas), 256, bytes, s, d_o, d_sN, cu, scale, N, T, HK, HV,
                        static_cast<uint8_t *>(ws), layout(N, T, HK, HV, D, true), static_cast<Tin *>(dv),
                        d_s0, status);
 }
@@ -843,13 +1152,7 @@ cudaError_t launch_typed(const void *v, const float *g, const float *beta, const
                          float scale, int N, int T, int HK, int HV, void *ws, const float *d_o,
                          const float *d_sN, void *dq, void *dk, void *dv, float *dg, float *dbeta,
                          float *d_s0, int *status, cudaStream_t s) {
-  cudaError_t e;
-  // The split of a head over CTAs is the forward's (kda_gdr_state.cu).
-  if (D == 64 || (long long)N * HV * 2 <= 148)
-    e = launch_reverse<Tin, D, 4>(cu, scale, N, T, HK, HV, ws, d_o, d_sN, dv, d_s0, status, s);
-  else
-    e = launch_reverse<Tin, D, D == 64 ? 4 : 8>(cu, scale, N, T, HK, HV, ws, d_o, d_sN, dv, d_s0,
-                                                status, s);
+  cudaError_t e = launch_reverse<Tin, D>(cu, scale, N, T, HK, HV, ws, d_o, d_sN, dv, d_s0, status, s);
   if (e != cudaSuccess) return e;
   auto kern = gdr_local_kernel<Tin, D>;
   const int bytes = (int)LocalSmem<D>::kBytes;
