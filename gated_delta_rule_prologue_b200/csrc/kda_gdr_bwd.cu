@@ -22,7 +22,7 @@
 // Per value head and chunk at D = 128 the reverse pass is 504 MMAs per 16 value channels, the local
 // pass about 1000 per warp (8 warps); a chunk of the local pass reads 270 KB.  The local pass keeps S and dS' as split
 // fp16 rows in shared memory (128 KB) with K, Q, U and dO or X, one persistent CTA per SM.
-// Bounds: the reverse pass a chain's latency, 5.8 us a chunk (64 chains of 32 chunks on 128 SMs: 186 us);
+// Bounds: the reverse pass a chain's latency, 5.6 us a chunk (64 chains of 32 chunks on 128 SMs: 180 us);
 // the local pass the latency of its steps with two warps per SM quarter
 // (the tensor pipe is busy 34% of the time, 28% of the issue slots), 26 us a chunk and SM: 2048 chunks
 // 372 us, 629 MB.  16 warps per CTA: 428.
@@ -290,7 +290,7 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
 // The form of 64 value channels per CTA: warps 0-3 carry the chain, and warps 4-7 compute, one chunk ahead
 // of them, what does not depend on dS': (P^T dO~)^T and ((G dO~)^T Q).  A lane of warp w + 4 holds the
 // elements that the same lane of warp w adds, so they pass through shared memory lane by lane.  The
-// chain is 316 of the 504 MMAs: 5.8 us a chunk, 6.9 with all of them on four warps (4 x 2048 tokens, 16
+// chain is 316 of the 504 MMAs: 5.6 us a chunk, 6.9 with all of them on four warps (4 x 2048 tokens, 16
 // heads: 749 -> 716 us).
 template <int D> struct PairSmem {
   static constexpr int kLd = 64 + 4;                            // row stride of the dO tile
@@ -1126,8 +1126,8 @@ template <typename Tin, int D>
 cudaError_t launch_reverse(const int32_t *cu, float scale, int N, int T, int HK, int HV, void *ws,
                            const float *d_o, const float *d_sN, void *dv, float *d_s0, int *status,
                            cudaStream_t s) {
-  // Two CTAs of 64 value channels per head as long as all of them run at once, else whole heads (8.2 us a
-  // chunk where two CTAs on the same SM in turn take 11.6), as the forward (kda_gdr_state.cu).
+  // Two CTAs of 64 value channels per head as long as all of them run at once (5.6 us a chunk), else whole
+  // heads (10.4 us; the two halves on one SM in turn 11.2), as the forward (kda_gdr_state.cu).
   const bool whole = D == 128 && (long long)N * HV * 2 > 148;
   void (*kern)(const float *, const float *, const int32_t *, float, int, int, int, int, uint8_t *, Layout,
                Tin *, float *, int *) = gdr_reverse_pair_kernel<Tin, D>;

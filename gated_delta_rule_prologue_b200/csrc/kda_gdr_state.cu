@@ -501,7 +501,7 @@ cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float sc
   const Layout lay = layout(N, T, HK, HV, D, bwd);
   // D = 128: two CTAs of four warps per head, one per SM, if they all run at once, or else, and for
   // segments, which fill the SMs by themselves, the tcgen05 form with one CTA per head.  Microseconds a
-  // chunk, here and there: with the read-out 4.9 and 5.3, kept for the backward 3.9 and 5.3, maps 4.1 and 4.2.
+  // chunk, here and there: with the read-out 4.9 and 5.3, kept for the backward 3.9 and 6.3, maps 4.1 and 4.2.
   const bool tensor_memory = D == 128 && (lay.seg_chunks || (long long)N * HV * 2 > 148);
   const kda_dtype dt = std::is_same<Tin, __half>::value ? KDA_F16 : KDA_BF16;
   if (bwd)
