@@ -106,6 +106,7 @@ struct Layout {
   size_t kq, tp;                 // records
   size_t state, dstate, u, x;    // backward: per chunk fp32 S and dS' (key-major: [key][value channel]),
                                  // U and X [64][D]
+  size_t scales;                 // backward: per chunk the scales of the value channels of S, then of dS'
   int seg_chunks;                // forward: chunks per segment, or 0
   size_t seg_m, seg_b, seg_e;    // and per segment M (map_bytes), fp32 B and first state, like a state
   size_t bytes;
@@ -120,7 +121,8 @@ inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
   l.dstate = l.state + (bwd ? sq : 0);
   l.u = l.dstate + (bwd ? sq : 0);
   l.x = l.u + (bwd ? rows : 0);
-  l.seg_m = l.x + (bwd ? rows : 0);
+  l.scales = l.x + (bwd ? rows : 0);
+  l.seg_m = l.scales + (bwd ? n * HV * 2 * (size_t)D * 4 : 0);
   l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV, D);
   const size_t segs = l.seg_chunks ? (size_t)segment_slots(N, T, l.seg_chunks) * HV : 0;
   const size_t seg = segs * D * D * 4;
@@ -408,7 +410,7 @@ template <int NT> __device__ __forceinline__ void zero(float (&c)[NT][4]) {
 
 // A matrix of fp32 rows of D values becomes, in its place, one of split rows: per row D fp16 hi,
 // then D fp16 lo (4 D bytes as before), the 16-byte pieces of each XOR-swizzled by the row, so that
-// ldmatrix reads eight rows without bank conflicts.  A warp owns whole rows: no block barrier.
+// ldmatrix reads eight rows without bank conflicts.
 template <int D> __device__ __forceinline__ uint32_t row_off(int row, int c8) {
   return (uint32_t)(row * 4 * D + ((c8 ^ (row & 7)) << 4));
 }
@@ -431,31 +433,6 @@ __device__ __forceinline__ void load_rows_bt(uint32_t (&r)[4], uint32_t base, in
   const int lane = threadIdx.x & 31, m = lane >> 3;
   ldsm4t(r, base + row_off<D>(k0 + (m & 1) * 8 + (lane & 7), (n0 >> 3) + (m >> 1)) + (lo ? 2 * D : 0));
 }
-// A warp splits its `rows` rows from row0 on (a multiple of four accesses of 128 / D rows).
-template <int D>
-__device__ __forceinline__ void split_rows_in_place(uint8_t *base, int row0, int rows, float inv) {
-  constexpr int LR = D / 4, RP = 32 / LR;  // lanes per row, rows per warp access
-  const int lane = threadIdx.x & 31, rl = lane / LR, cl = lane % LR;
-#pragma unroll 1
-  for (int i = 0; i < rows; i += 4 * RP) {
-    float4 x[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      x[k] = *reinterpret_cast<const float4 *>(base + (row0 + i + k * RP + rl) * 4 * D + 16 * cl);
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint2 hi, lo;
-      split2(x[k].x, x[k].y, inv, hi.x, lo.x);
-      split2(x[k].z, x[k].w, inv, hi.y, lo.y);
-      const uint32_t o = row_off<D>(row0 + i + k * RP + rl, cl >> 1) + 8 * (cl & 1);
-      *reinterpret_cast<uint2 *>(base + o) = hi;
-      *reinterpret_cast<uint2 *>(base + o + 2 * D) = lo;
-    }
-    __syncwarp();
-  }
-}
-
 }  // namespace gdr
 
 // Host side (kda_gdr_*.cu), called by kda_api.cu; the *_tc form is launch_gdr_state's for D = 128.

@@ -23,9 +23,9 @@
 // pass about 1000 per warp (8 warps); a chunk of the local pass reads 270 KB.  The local pass keeps S and dS' as split
 // fp16 rows in shared memory (128 KB) with K, Q, U and dO or X, one persistent CTA per SM.
 // Bounds: the reverse pass a chain's latency, 5.6 us a chunk (64 chains of 32 chunks on 128 SMs: 180 us);
-// the local pass the latency of its steps with two warps per SM quarter
-// (the tensor pipe is busy 34% of the time, 28% of the issue slots), 26 us a chunk and SM: 2048 chunks
-// 372 us, 629 MB.  16 warps per CTA: 428.
+// the local pass the latency of its steps with two warps per SM quarter (the tensor pipe is busy about 36%
+// of the time, 30% of the issue slots), 25 us a chunk and SM: 2048 chunks 350 us, 629 MB.  372 us with the
+// scales, g and beta loaded when an item starts instead of one ahead; 428 with 16 warps per CTA then.
 #include "kda_gdr.cuh"
 #include "kda_tcgen05.cuh"
 
@@ -128,6 +128,11 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
     zero(du);
     Scale a0, a1;
     row_scales(s, a0, a1);
+    if ((lane & 3) == 0) {
+      float *p = reinterpret_cast<float *>(ws + lay.scales) + rec * 2 * D + D + row;
+      p[0] = a0.s;
+      p[8] = a1.s;
+    }
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       uint32_t hi[4], lo[4];
@@ -488,6 +493,11 @@ gdr_reverse_pair_kernel(const float *__restrict__ d_o, const float *d_sN, const 
     zero(du);
     Scale a0, a1, r0, r1;
     row_scales(s, a0, a1);
+    if ((lane & 3) == 0) {
+      float *p = reinterpret_cast<float *>(ws + lay.scales) + rec * 2 * D + D + row;
+      p[0] = a0.s;
+      p[8] = a1.s;
+    }
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       uint32_t hi[4], lo[4];
@@ -603,10 +613,11 @@ template <int D> struct LocalSmem {
     float cross[8];
   };
   struct Small {
+    alignas(16) float scales[2][D];      // of the value channels of S and of dS', as the passes left them
     alignas(16) float2 gamma[C];
     float beta[C], us[C], as[C], xv[C];  // us, as: scales of U's and of dO's or X's rows
     float red[8][2];
-    float kq[2];
+    alignas(16) float kq[4];             // the tile's two scales
     uint64_t states, rest;               // S and dS' have landed; U (and K and Q) have
   };
   static constexpr uint32_t kBytes = kSmall + sizeof(Small);
@@ -652,6 +663,45 @@ __device__ __forceinline__ float2 tile_pair(const uint8_t *tile, int row, int c8
 
 // Persistent: a CTA takes every gridDim.x-th (chunk, key head).  S and dS' of the next (chunk,
 // head) are fetched as soon as this one's have been used, behind the products that are left.
+// A warp splits its rows of S and of dS' in their places (row_off; whole rows, so no block barrier), and
+// sums their products on the way.  `rows` is a multiple of four accesses of 128 / D rows.
+template <int D>
+__device__ __forceinline__ float split_states_in_place(uint8_t *s, uint8_t *ds, int row0, int rows, float inv,
+                                                       float dinv) {
+  constexpr int LR = D / 4, RP = 32 / LR;  // lanes per row, rows per warp access
+  const int lane = threadIdx.x & 31, rl = lane / LR, cl = lane % LR;
+  float cross = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < rows; i += 4 * RP) {
+    float4 x[2][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = (row0 + i + k * RP + rl) * 4 * D + 16 * cl;
+      x[0][k] = *reinterpret_cast<const float4 *>(s + at);
+      x[1][k] = *reinterpret_cast<const float4 *>(ds + at);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 &a = x[0][k], &b = x[1][k];
+      cross += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+      const uint32_t o = row_off<D>(row0 + i + k * RP + rl, cl >> 1) + 8 * (cl & 1);
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        const float4 &y = x[which][k];
+        uint8_t *to = (which ? ds : s) + o;
+        uint2 hi, lo;
+        split2(y.x, y.y, which ? dinv : inv, hi.x, lo.x);
+        split2(y.z, y.w, which ? dinv : inv, hi.y, lo.y);
+        *reinterpret_cast<uint2 *>(to) = hi;
+        *reinterpret_cast<uint2 *>(to + 2 * D) = lo;
+      }
+    }
+    __syncwarp();
+  }
+  return cross;
+}
+
 template <typename Tin, int D>
 __global__ void __launch_bounds__(kLocalThreads, 1)
 gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
@@ -688,9 +738,10 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
   // One thread: S and dS' of a (chunk, head), 4 D^2 bytes each as the state passes left them.
   auto fetch_states = [&](long long item, int j) {
     const size_t rec = (size_t)(item / HK) * HV + item % HK * group + j;
-    tc::mbar_arrive_expect_tx(&sm.states, 2 * D * D * 4);
+    tc::mbar_arrive_expect_tx(&sm.states, 2 * D * D * 4 + 2 * D * 4);
     tc::bulk_load(smem + Sm::kS, ws + lay.state + rec * D * D * 4, D * D * 4, &sm.states);
     tc::bulk_load(smem + Sm::kD, ws + lay.dstate + rec * D * D * 4, D * D * 4, &sm.states);
+    tc::bulk_load(sm.scales, ws + lay.scales + rec * 2 * D * 4, 2 * D * 4, &sm.states);
   };
   // A warp's 8 of 64 rows, held in registers, with a scale per row.
   constexpr int kHeld = 8 / RP;
@@ -721,6 +772,19 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
     store_rows(x, base, scales);
   };
 
+  // A (chunk, head)'s g (warp 7) or beta (warp 6), an item ahead like its states.
+  float small[2];
+  auto fetch_small = [&](int t0, int len, int h) {
+    if (warp == 7) {
+      const float *g0 = g + (size_t)t0 * HV + h;
+      small[0] = load_g(g0, HV, 2 * lane, len);
+      small[1] = load_g(g0, HV, 2 * lane + 1, len);
+    } else if (warp == 6) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        small[i] = lane + 32 * i < len ? __ldg(beta + (size_t)(t0 + lane + 32 * i) * HV + h) : 0.f;
+    }
+  };
   if (tid == 0) {
     tc::mbar_init(&sm.states, 1);
     tc::mbar_init(&sm.rest, 1);
@@ -730,6 +794,7 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
   uint32_t par = 0;  // of both barriers: one phase each per (chunk, head)
   long long item = next_item(blockIdx.x);
   if (tid == 0 && item < items) fetch_states(item, 0);
+  if (item < items) fetch_small(bos + c * C, min(C, eos - bos - c * C), (int)(item % HK) * group);
   while (item < items) {
     const long long slot = item / HK;
     const int hk = (int)(item % HK);
@@ -747,13 +812,11 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
       // U (with the first head K and Q) and dO on their way behind S and dS'.
       if (tid == 0) {
         const uint8_t *kq = ws + lay.kq + (size_t)(slot * HK + hk) * kq_bytes(D);
-        tc::mbar_arrive_expect_tx(&sm.rest, C * D * 4 + (j == 0 ? kq_tile_bytes(D) : 0));
+        tc::mbar_arrive_expect_tx(&sm.rest, C * D * 4 + (j == 0 ? kq_tile_bytes(D) + 16 : 0));
         tc::bulk_load(smem + Sm::kU, Ug, C * D * 4, &sm.rest);
         if (j == 0) {
           tc::bulk_load(smem, kq, kq_tile_bytes(D), &sm.rest);
-          const float2 f = *reinterpret_cast<const float2 *>(kq + kq_tile_bytes(D));
-          sm.kq[0] = f.x;
-          sm.kq[1] = f.y;
+          tc::bulk_load(sm.kq, kq + kq_tile_bytes(D), 16, &sm.rest);
         }
       }
 #pragma unroll
@@ -763,14 +826,10 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
       }
       cp_commit();
       if (warp == 7) {
-        const float *g0 = g + (size_t)t0 * HV + h;
-        gamma_of(load_g(g0, HV, 2 * lane, len), load_g(g0, HV, 2 * lane + 1, len), sm.gamma);
+        gamma_of(small[0], small[1], sm.gamma);
       } else if (warp == 6) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = lane + 32 * i;
-          sm.beta[t] = t < len ? __ldg(beta + (size_t)(t0 + t) * HV + h) : 0.f;
-        }
+        sm.beta[lane] = small[0];
+        sm.beta[lane + 32] = small[1];
       }
       // S and dS' with one power of two per matrix, and <dS', S>.
       if (!tc::wait_all(&sm.states, par, status)) {
@@ -782,22 +841,19 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
         __syncthreads();
         return;
       }
-      float cross = 0.f;
       float2 big = make_float2(0.f, 0.f);
-      constexpr int kRows = D / 8;  // of each matrix per warp
-#pragma unroll 4
-      for (int i = 0; i < kRows; i += RP) {
-        const uint32_t o = (kRows * warp + i + rl) * 4 * D + 16 * cl;
-        const float4 a = *reinterpret_cast<const float4 *>(smem + Sm::kS + o);
-        const float4 b = *reinterpret_cast<const float4 *>(smem + Sm::kD + o);
-        big.x = max_abs4(a, big.x);
-        big.y = max_abs4(b, big.y);
-        cross += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+      if (lane < D / 4) {
+        big.x = max_abs4(reinterpret_cast<const float4 *>(sm.scales[0])[lane], 0.f);
+        big.y = max_abs4(reinterpret_cast<const float4 *>(sm.scales[1])[lane], 0.f);
       }
-      big = block_max2(big.x, big.y, sm.red);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        big.x = fmaxf(big.x, __shfl_xor_sync(0xffffffffu, big.x, off));
+        big.y = fmaxf(big.y, __shfl_xor_sync(0xffffffffu, big.y, off));
+      }
       const Scale ss = scale_of(big.x), ds = scale_of(big.y);
-      split_rows_in_place<D>(smem + Sm::kS, kRows * warp, kRows, ss.inv);
-      split_rows_in_place<D>(smem + Sm::kD, kRows * warp, kRows, ds.inv);
+      constexpr int kRows = D / 8;  // of each matrix per warp
+      float cross = split_states_in_place<D>(smem + Sm::kS, smem + Sm::kD, kRows * warp, kRows, ss.inv, ds.inv);
       cp_wait<0>();  // this thread's part of its own warp's rows of dO
       __syncwarp();
       split_own(Sm::kA, sm.as);
@@ -1005,9 +1061,12 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
       const float2 most = block_max2(bigw, bigm, sm.red);  // also: S, dS', U, X have been read
       if (j + 1 < group) {
         if (tid == 0) fetch_states(item, j + 1);
+        fetch_small(t0, len, h + 1);
       } else {
         following = next_item(item + gridDim.x);  // bos, eos and c are the next item's from here on
         if (tid == 0 && following < items) fetch_states(following, 0);
+        if (following < items)
+          fetch_small(bos + c * C, min(C, eos - bos - c * C), (int)(following % HK) * group);
       }
       const Scale sw = scale_of(most.x), sn = scale_of(most.y);
 #pragma unroll
@@ -1085,19 +1144,19 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
                  ((double)sums.cols[0][r] + sums.cols[1][r] + sums.cols[2][r] + sums.cols[3][r]);
           e += et;
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) e += __shfl_xor_sync(0xffffffffu, e, off);
         float t = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) t += sums.cross[i];
         const float2 gl = sm.gamma[C - 1];
-        if (lane == 31) d[1] += e + (double)(ex2_approx(gl.x + gl.y) * t);
+        // The last token's share is in every sum from a token to the end.
         double s = d[0] + d[1];
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const double o = __shfl_down_sync(0xffffffffu, s, off);
+          e += __shfl_xor_sync(0xffffffffu, e, off);
           if (lane + off < 32) s += o;
         }
+        s += e + (double)(ex2_approx(gl.x + gl.y) * t);
         if (2 * lane < len) dg[(size_t)(t0 + 2 * lane) * HV + h] = (float)s;
         if (2 * lane + 1 < len) dg[(size_t)(t0 + 2 * lane + 1) * HV + h] = (float)(s - d[0]);
       }
