@@ -17,7 +17,10 @@
 //               records and of V
 // Hand-over is by mbarriers in both directions (no block barrier inside the loop); every wait is
 // bounded, and a wait that ran out ends the loop of the warp that saw it, after which the others'
-// waits run out too.
+// waits run out too.  A wait names a parity, so no barrier may complete its next phase before every
+// warp that waits for this one has seen it: a stage's two barriers hold one another (what is loaded
+// next waits for `empty`), s_ready is waited for by the read-out only where q_read holds the chain
+// until then, and the chain's first warp sees u_ready of the last chunk before it arrives at r_ready.
 //
 // Triangular T and P: the k-step of tokens 16 k .. only reaches token columns from 16 k on, so its
 // MMA is 64 - 16 k columns wide.
@@ -56,7 +59,7 @@ constexpr uint32_t kStage = kStV + C * D * 2;
 static_assert(kq_bytes(D) <= kStTp && kTpBytes <= 34816 && kStage % 1024 == 0, "stage plan");
 
 struct Small {
-  uint64_t full[2], s_ready, r_ready, w_ready, q_read, u_ready, out_done, d_s, d_u, d_acc, d_pu;
+  uint64_t full[2], empty[2], s_ready, r_ready, w_ready, q_read, u_ready, out_done, d_s, d_u, d_acc, d_pu;
   uint64_t met[4][3];                 // per 32 value channels: the two warps' largest S, R, W
   uint32_t tmem;
   int dead;
@@ -192,6 +195,8 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
     if (lane == 0) {
       tc::mbar_init(&sm.full[0], 1);
       tc::mbar_init(&sm.full[1], 1);
+      tc::mbar_init(&sm.empty[0], kChainWarps);
+      tc::mbar_init(&sm.empty[1], kChainWarps);
       tc::mbar_init(&sm.s_ready, kChainWarps);
       tc::mbar_init(&sm.r_ready, kChainWarps);
       tc::mbar_init(&sm.w_ready, kChainWarps);
@@ -331,11 +336,11 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       store_split(x, rs.inv, tl + TM_W + 16 * half, tl + TM_W + 32 + 16 * half);
       if (half == 0) sm.r_scale[par][row] = rs.s;
       tmem_wait_st();
+      // The last chunk's U has been read; and no warp of the read-out is left behind that chunk's r_ready.
+      if (warp == 0 && kRole != kMap && c > 0 && !(ok = wait(&sm.u_ready, par ^ 1, sm, status))) break;
       warp_arrive(&sm.r_ready);
       if (warp == 0) {
         if (!(ok = wait(&sm.r_ready, par, sm, status))) break;
-        // the last chunk's U has been read
-        if (kRole != kMap && c > 0 && !(ok = wait(&sm.u_ready, par ^ 1, sm, status))) break;
         mma_triangular(tm + TM_U, tm + TM_W, tc::sdesc(st32 + kStTp + kT_HI, 16, 1024));
         commit(leader, &sm.d_u);
       }
@@ -371,6 +376,7 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
         commit(leader, &sm.d_acc);
       }
       if (!(ok = wait(&sm.d_acc, par, sm, status))) break;
+      warp_arrive(&sm.empty[par]);
       const float f = wsc.s * ks;
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
@@ -421,16 +427,21 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
       const int t0 = bos + c * C, len = min(C, eos - t0);
       if constexpr (kRole == kMap) {  // nothing to read out: a stage is free when the chain has left it
         if (warp > kChainWarps) break;
-        if (!(ok = wait(&sm.s_ready, par, sm, status))) break;
-        if (c > 0 && c + 1 < chunks) load(c + 1);
+        if (c > 0 && c + 1 < chunks) {
+          if (!(ok = wait(&sm.empty[par ^ 1], ((c - 1) >> 1) & 1, sm, status))) break;
+          load(c + 1);
+        }
         continue;
       }
       if (!(ok = wait(&sm.full[par], (c >> 1) & 1, sm, status))) break;
-      if (!(ok = wait(&sm.s_ready, par, sm, status))) break;
-      // Chunk c - 1's read-out is done, and with it every reader of its stage.
+      if (kRole == kOut && !(ok = wait(&sm.s_ready, par, sm, status))) break;
+      // Chunk c - 1's read-out is done, and the chain has left its stage.
       if (warp == kChainWarps && c > 0) {
         if (!(ok = wait(&sm.out_done, par ^ 1, sm, status))) break;
-        if (c + 1 < chunks) load(c + 1);
+        if (c + 1 < chunks) {
+          if (!(ok = wait(&sm.empty[par ^ 1], ((c - 1) >> 1) & 1, sm, status))) break;
+          load(c + 1);
+        }
       }
       float q[kRole == kOut ? C : 1];
       if constexpr (kRole == kOut) {
