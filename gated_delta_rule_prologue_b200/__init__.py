@@ -19,6 +19,10 @@ Tensor conventions (all contiguous, on the current CUDA device):
   conv cache           [N, 3, 3*H*D]   activation dtype, oldest row first
   cu_seqlens           [N+1]           int32
 
+A call runs on torch's current stream, or on ``stream``.  Scratch and outputs that a call allocates come
+from that stream's memory, as under ``torch.cuda.stream(stream)``: before another stream uses such an
+output, it waits for ``stream``, and the output outlives that use or is given to ``record_stream``.
+
 Gated delta rule with one decay per head (``kda_gdr_*``): q, k [T, HK, D], v, o [T, HV, D],
 g and beta [T, HV] float32, states [N, HV, D, D] float32, HV a multiple of HK.
 """
@@ -214,6 +218,22 @@ def _need(t, name, dtype=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+_STREAM = torch.cuda.Stream
+
+
+def _new(shape, dtype, device, stream):
+    """An uninitialised tensor for a call on ``stream`` (None: the current one), taken from that
+    stream's memory.  torch's allocator orders a block's uses by the stream it was allocated on: a
+    block of the current stream might still be in use there when the call begins, and would be
+    given away there, once its tensor is gone, while the call still works in it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, _STREAM):  # another library's, by its handle
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def kda_version() -> str:
     return lib.kda_version().decode()
 
@@ -313,7 +333,7 @@ def kda_chunk_fwd(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=None
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
         nbytes = kda_chunk_fwd_workspace_bytes(N, T, H, Dk, Dv, chunk, q.dtype)
-        workspace = (torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None)
+        workspace = (_new(nbytes, torch.uint8, q.device, stream) if nbytes else None)
     if workspace is None:
         _check(lib.kda_chunk_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
                                  _ptr(initial_state), _ptr(cu_seqlens), N, T, H, Dk, Dv, chunk,
@@ -347,7 +367,7 @@ def _chunk_fwd_windowed(q, k, v, g, beta, o, scale, initial_state, final_state, 
             raise ValueError(f"workspace must be 'auto' or a tensor, not {workspace!r}")
         nbytes = kda_chunk_fwd_windowed_workspace_bytes(N, T, H, Dk, Dv, chunk, q.dtype,
                                                         window_chunks)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(nbytes, 1), torch.uint8, q.device, stream)
     _need(workspace, "workspace", torch.uint8)
     _check(lib.kda_chunk_fwd_windowed_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                          float(scale), _ptr(initial_state), _ptr(cu_seqlens), N,
@@ -372,7 +392,7 @@ def _chunk_fwd_segmented(q, k, v, g, beta, o, scale, initial_state, final_state,
             raise ValueError(f"workspace must be 'auto' or a tensor, not {workspace!r}")
         nbytes = kda_chunk_fwd_segmented_workspace_bytes(N, T, H, Dk, Dv, chunk, q.dtype,
                                                          segment_chunks)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(nbytes, 1), torch.uint8, q.device, stream)
     _need(workspace, "workspace", torch.uint8)
     _check(lib.kda_chunk_fwd_segmented_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                                           float(scale), _ptr(initial_state), _ptr(cu_seqlens), N,
@@ -404,13 +424,13 @@ def kda_chunk_bwd(q, k, v, g, beta, d_o, *, scale: float = 1.0, initial_state=No
     Dv = v.shape[2]
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
     dev = q.device
-    dq = torch.empty((T, H, Dk), device=dev) if dq is None else dq
-    dk = torch.empty((T, H, Dk), device=dev) if dk is None else dk
-    dv = torch.empty((T, H, Dv), device=dev) if dv is None else dv
-    dg = torch.empty((T, H, Dk), device=dev) if dg is None else dg
-    dbeta = torch.empty((T, H), device=dev) if dbeta is None else dbeta
+    dq = _new((T, H, Dk), torch.float32, dev, stream) if dq is None else dq
+    dk = _new((T, H, Dk), torch.float32, dev, stream) if dk is None else dk
+    dv = _new((T, H, Dv), torch.float32, dev, stream) if dv is None else dv
+    dg = _new((T, H, Dk), torch.float32, dev, stream) if dg is None else dg
+    dbeta = _new((T, H), torch.float32, dev, stream) if dbeta is None else dbeta
     if d_initial_state is None and want_d_initial_state:
-        d_initial_state = torch.empty((N, H, Dv, Dk), device=dev)
+        d_initial_state = _new((N, H, Dv, Dk), torch.float32, dev, stream)
     for t, n in ((dq, "dq"), (dk, "dk"), (dv, "dv"), (dg, "dg"), (dbeta, "dbeta"),
                  (d_initial_state, "d_initial_state")):
         _need(t, n, torch.float32)
@@ -418,7 +438,7 @@ def kda_chunk_bwd(q, k, v, g, beta, d_o, *, scale: float = 1.0, initial_state=No
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto' or a tensor, not {workspace!r}")
         nbytes = kda_chunk_bwd_workspace_bytes(N, T, H, Dk, Dv, chunk, q.dtype)
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        workspace = _new(max(nbytes, 1), torch.uint8, dev, stream)
     _need(workspace, "workspace", torch.uint8)
     _check(lib.kda_chunk_bwd_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale),
                                 _ptr(initial_state), _ptr(cu_seqlens), N, T, H, Dk, Dv, chunk,
@@ -440,15 +460,15 @@ def kda_chunk_map(q, k, v, g, beta, *, cu_seqlens=None, chunk: int = 64, M=None,
     T, H, Dk = q.shape
     Dv = v.shape[2]
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
-    M = torch.empty((N, H, Dk, Dk), device=q.device) if M is None else M
-    B = torch.empty((N, H, Dv, Dk), device=q.device) if B is None else B
+    M = _new((N, H, Dk, Dk), torch.float32, q.device, stream) if M is None else M
+    B = _new((N, H, Dv, Dk), torch.float32, q.device, stream) if B is None else B
     _need(M, "M", torch.float32)
     _need(B, "B", torch.float32)
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto' or a tensor, not {workspace!r}")
         nbytes = int(lib.kda_chunk_map_workspace_bytes(N, T, H, Dk, Dv, chunk, _DTYPES[q.dtype]))
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(max(nbytes, 1), torch.uint8, q.device, stream)
     _need(workspace, "workspace", torch.uint8)
     _check(lib.kda_chunk_map_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), N,
                                 T, H, Dk, Dv, chunk, _dtype(q), _ptr(M), _ptr(B), _ptr(workspace),
@@ -461,7 +481,7 @@ def kda_state_compose(M, B, E_in, E_out=None, stream=None):
     for t, n in ((M, "M"), (B, "B"), (E_in, "E_in")):
         _need(t, n, torch.float32)
     N, H, D = B.shape[0], B.shape[1], B.shape[2]
-    E_out = torch.empty_like(B) if E_out is None else E_out
+    E_out = _new(B.shape, B.dtype, B.device, stream) if E_out is None else E_out
     _need(E_out, "E_out", torch.float32)
     _check(lib.kda_state_compose(_ptr(M), _ptr(B), _ptr(E_in), _ptr(E_out), N, H, D,
                                  _stream(stream)))
@@ -519,7 +539,7 @@ def kda_prologue_chunk_fwd(x, conv_w, g, beta, o, *, H: int, D: int, scale: floa
                 raise ValueError(f"workspace must be 'auto' or a tensor, not {workspace!r}")
             nbytes = kda_chunk_fwd_windowed_workspace_bytes(N, T, H, D, D, 64, x.dtype,
                                                             int(window_chunks))
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=x.device)
+            workspace = _new(max(nbytes, 1), torch.uint8, x.device, stream)
         _need(workspace, "workspace", torch.uint8)
         _check(lib.kda_prologue_chunk_fwd_windowed_ws(
             _ptr(x), _ptr(conv_w), _ptr(cache_in), _ptr(cache_out), _ptr(g), _ptr(beta),
@@ -531,7 +551,7 @@ def kda_prologue_chunk_fwd(x, conv_w, g, beta, o, *, H: int, D: int, scale: floa
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
         nbytes = kda_chunk_fwd_workspace_bytes(N, T, H, D, D, 64, x.dtype)
-        workspace = (torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None)
+        workspace = (_new(nbytes, torch.uint8, x.device, stream) if nbytes else None)
     if workspace is None:
         _check(lib.kda_prologue_chunk_fwd(_ptr(x), _ptr(conv_w), _ptr(cache_in), _ptr(cache_out),
                                           _ptr(g), _ptr(beta), float(scale), _ptr(initial_state),
@@ -559,12 +579,12 @@ def kda_decode_step(x, conv_w, conv_cache, g, beta, state, o, *, H: int, D: int,
                                _stream(stream)))
 
 
-def _auto_workspace(workspace, N, T, H, D, dtype, device):
+def _auto_workspace(workspace, N, T, H, D, dtype, device, stream):
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError(f"workspace must be 'auto' or a tensor, not {workspace!r}")
         nbytes = kda_chunk_fwd_workspace_bytes(N, T, H, D, D, 64, dtype)
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        return _new(max(nbytes, 16), torch.uint8, device, stream)
     _need(workspace, "workspace", torch.uint8)
     return workspace
 
@@ -585,7 +605,7 @@ def kda_chunk_fwd_gated(q, k, v, g_raw, beta, o, *, A_log=None, dt_bias=None,
     T, H, Dk = q.shape
     Dv = v.shape[2]
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
-    workspace = _auto_workspace(workspace, N, T, H, Dk, q.dtype, q.device)
+    workspace = _auto_workspace(workspace, N, T, H, Dk, q.dtype, q.device, stream)
     _check(lib.kda_chunk_fwd_gated_ws(_ptr(q), _ptr(k), _ptr(v), _ptr(g_raw), _ptr(A_log),
                                       _ptr(dt_bias), float(lower_bound), _ptr(beta), float(scale),
                                       _ptr(initial_state), _ptr(cu_seqlens), N, T, H, Dk, Dv,
@@ -608,7 +628,7 @@ def kda_prologue_chunk_fwd_gated(x, conv_w, g_raw, beta, o, *, H: int, D: int, A
     _need(cu_seqlens, "cu_seqlens", torch.int32)
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
     T = x.shape[0]
-    workspace = _auto_workspace(workspace, N, T, H, D, x.dtype, x.device)
+    workspace = _auto_workspace(workspace, N, T, H, D, x.dtype, x.device, stream)
     _check(lib.kda_prologue_chunk_fwd_gated_ws(_ptr(x), _ptr(conv_w), _ptr(cache_in),
                                                _ptr(cache_out), _ptr(g_raw), _ptr(A_log),
                                                _ptr(dt_bias), float(lower_bound), _ptr(beta),
@@ -685,7 +705,7 @@ def _stream_of(stream, device):
     return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
-def _scratch(workspace, nbytes, device, like):
+def _scratch(workspace, nbytes, device, like, stream):
     """Address and bytes of a workspace ("auto": ``nbytes`` from torch's caching allocator); the
     third value keeps it alive until the call has been made."""
     if workspace is None:
@@ -695,7 +715,7 @@ def _scratch(workspace, nbytes, device, like):
             raise ValueError(f"workspace must be 'auto', None or a tensor, not {workspace!r}")
         if nbytes == 0:
             return None, 0, None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        workspace = _new(nbytes, torch.uint8, like.device, stream)
     n = workspace.numel()
     return _p(workspace, "workspace", (n,), torch.uint8, device), n, workspace
 
@@ -780,7 +800,7 @@ def kda_gdr_chunk_fwd(q, k, v, g, beta, o, *, scale: float = 1.0, initial_state=
     nbytes = 0
     if isinstance(workspace, str):
         nbytes = lib.kda_gdr_chunk_fwd_workspace_bytes(*sizes)
-    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, q)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, q, stream)
     _check(lib.kda_gdr_chunk_fwd_ws(*x, scale, s0, cu, *sizes, op, sN, ws, nbytes,
                                     _stream_of(stream, dev)))
 
@@ -802,17 +822,17 @@ def kda_gdr_chunk_bwd(q, k, v, g, beta, d_o, *, scale: float = 1.0, initial_stat
     N, T, HK, HV, D = _gdr_sizes(q, v, cu_seqlens)
     dev, f32, sq, dt = _cuda_device(q), torch.float32, (N, HV, D, D), _dtype(q)
     heads, qk, vo, act = (T, HV), (T, HK, D), (T, HV, D), q.dtype
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    dg = torch.empty_like(g) if dg is None else dg
-    dbeta = torch.empty_like(beta) if dbeta is None else dbeta
+    dq = _new(qk, act, q.device, stream) if dq is None else dq
+    dk = _new(qk, act, q.device, stream) if dk is None else dk
+    dv = _new(vo, act, q.device, stream) if dv is None else dv
+    dg = _new(heads, f32, q.device, stream) if dg is None else dg
+    dbeta = _new(heads, f32, q.device, stream) if dbeta is None else dbeta
     if d_initial_state is None and want_d_initial_state:
-        d_initial_state = torch.empty(sq, dtype=f32, device=q.device)
+        d_initial_state = _new(sq, f32, q.device, stream)
     nbytes = 0
     if workspace is not None and isinstance(workspace, str):
         nbytes = max(lib.kda_gdr_chunk_bwd_workspace_bytes(N, T, HK, HV, D, dt), 16)
-    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, q)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, q, stream)
     _check(lib.kda_gdr_chunk_bwd_ws(
         *_gdr_inputs(q, k, v, g, beta, T, HK, HV, D, dev), scale,
         _p(initial_state, "initial_state", sq, f32, dev),
@@ -853,7 +873,7 @@ def kda_prologue_bwd(x, conv_w, dq, dk, dv, dx, d_conv_w=None, *, H: int, D: int
     nbytes = 0
     if d_conv_w is not None and isinstance(workspace, str):
         nbytes = lib.kda_prologue_bwd_workspace_bytes(N, T, H, D, dt)
-    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, x)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, x, stream)
     _check(lib.kda_prologue_bwd(
         x.data_ptr(), conv_w.data_ptr(), _p(cache_in, "cache_in", (N, 3, C), act, dev),
         _p(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev), N, T, H, D, dt, _dtype(dq),
@@ -889,7 +909,7 @@ def kda_output_epilogue_bwd(o, gate, weight, d_out, d_o, d_gate, d_weight=None, 
     nbytes = 0
     if d_weight is not None and isinstance(workspace, str):
         nbytes = lib.kda_output_epilogue_bwd_workspace_bytes(T, H, D)
-    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, o)
+    ws, nbytes, _keep = _scratch(workspace, nbytes, dev, o, stream)
     _check(lib.kda_output_epilogue_bwd(
         o.data_ptr(), gate.data_ptr(), weight.data_ptr(), eps, d_out.data_ptr(), T, H, D,
         _dtype(gate), d_o.data_ptr(), d_gate.data_ptr(), _p(d_weight, "d_weight", (D,), f32, dev), ws,
