@@ -303,6 +303,12 @@ cudaError_t launch_behind(void (*kern)(P...), dim3 grid, unsigned threads, size_
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
+// Lets launches of a kernel ask for up to kBytes of dynamic shared memory.  The limit is the function's, not
+// the launch's: it is the same for every launch of an instance, because another host thread's call may
+// come between it and the launch that it is set for.
+template <int kBytes, typename... P> cudaError_t allow_smem(void (*kern)(P...)) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+}
 // Device addresses of the file-scope __device__ status word (kda_status.cu)
 // and of the fixed scratch of kda_chunk_fwd_static (kda_static.cu) on the
 // current device, looked up once per device.

@@ -96,7 +96,7 @@ __host__ __device__ constexpr uint32_t map_bytes(int D) { return (uint32_t)D * D
 // are SMs for all.  A chain is bound by its own latency, and two on an SM hold one another up: the CTAs
 // of a launch behind a kernel that is still ending are set up wherever there is room first (backward of
 // 4 x 2048 tokens, 16 heads: 753 us so, 813 us with the SMs shared).
-inline int chain_smem(int bytes, long long ctas) {
+constexpr int chain_smem(int bytes, long long ctas) {
   constexpr int kMoreThanHalf = 116 * 1024;
   return ctas <= 148 && bytes < kMoreThanHalf ? kMoreThanHalf : bytes;
 }

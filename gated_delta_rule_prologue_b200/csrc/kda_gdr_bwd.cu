@@ -1191,15 +1191,17 @@ cudaError_t launch_reverse(const int32_t *cu, float scale, int N, int T, int HK,
   void (*kern)(const float *, const float *, const int32_t *, float, int, int, int, int, uint8_t *, Layout,
                Tin *, float *, int *) = gdr_reverse_pair_kernel<Tin, D>;
   int bytes = (int)PairSmem<D>::kBytes;
+  cudaError_t e = cudaSuccess;
   long long ctas = (long long)N * HV * (D / 64);
   if constexpr (D == 128)
     if (whole) {
       kern = gdr_reverse_kernel<Tin, D>;
       bytes = (int)ReverseSmem<D>::kBytes;
       ctas = (long long)N * HV;
+      e = allow_smem<(int)ReverseSmem<D>::kBytes>(kern);
     }
+  if (!whole) e = allow_smem<(int)PairSmem<D>::kBytes>(kern);
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
   return launch_behind(kern, dim3((unsigned)ctas), 256, bytes, s, d_o, d_sN, cu, scale, N, T, HK, HV,
                        static_cast<uint8_t *>(ws), layout(N, T, HK, HV, D, true), static_cast<Tin *>(dv),
@@ -1214,8 +1216,8 @@ cudaError_t launch_typed(const void *v, const float *g, const float *beta, const
   cudaError_t e = launch_reverse<Tin, D>(cu, scale, N, T, HK, HV, ws, d_o, d_sN, dv, d_s0, status, s);
   if (e != cudaSuccess) return e;
   auto kern = gdr_local_kernel<Tin, D>;
-  const int bytes = (int)LocalSmem<D>::kBytes;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int bytes = (int)LocalSmem<D>::kBytes;
+  e = allow_smem<bytes>(kern);
   if (e != cudaSuccess) return e;
   const long long items = slots(N, T) * HK;
   const unsigned ctas = (unsigned)(items < 148 ? items : 148);  // one per SM

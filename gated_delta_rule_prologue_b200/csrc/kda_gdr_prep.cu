@@ -417,8 +417,8 @@ cudaError_t launch_typed(const void *q, const void *k, const float *g, const flo
                          const int32_t *cu, int N, int T, int HK, int HV, void *ws, bool bwd,
                          int *status, cudaStream_t s) {
   auto kern = gdr_prep_kernel<Tin, D>;
-  const int bytes = (int)sizeof(PrepSmem<D>);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int bytes = (int)sizeof(PrepSmem<D>);
+  const cudaError_t e = allow_smem<bytes>(kern);
   if (e != cudaSuccess) return e;
   const long long ctas = slots(N, T) * HV;
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;

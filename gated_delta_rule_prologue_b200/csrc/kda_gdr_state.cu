@@ -492,8 +492,9 @@ cudaError_t launch_role(const void *v, const float *s0, const int32_t *cu, float
   const long long units = kRole != kKeep && lay.seg_chunks ? segment_slots(N, T, lay.seg_chunks) : N;
   const long long ctas = units * HV * (D / (16 * NW)) * (kRole == kMap ? 2 : 1);
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
-  const int bytes = chain_smem((int)StateSmem<D, NW, kRole>::kBytes, ctas);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int kBytes = (int)StateSmem<D, NW, kRole>::kBytes;
+  const int bytes = chain_smem(kBytes, ctas);
+  const cudaError_t e = allow_smem<chain_smem(kBytes, 1)>(kern);  // the most that any launch asks for
   if (e != cudaSuccess) return e;
   return launch_behind(kern, dim3((unsigned)ctas), NW * 32, bytes, s, static_cast<const Tin *>(v), s0,
                        cu, scale, N, T, HK, HV, static_cast<uint8_t *>(ws), lay, o, sN, status);
@@ -521,8 +522,8 @@ cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float sc
       e = launch_role<Tin, D, 4, kMap>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
     if (e != cudaSuccess) return e;
     auto scan = gdr_scan_kernel<D>;
-    const int bytes = (int)ScanSmem<D>::kBytes;
-    e = cudaFuncSetAttribute(scan, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    constexpr int bytes = (int)ScanSmem<D>::kBytes;
+    e = allow_smem<bytes>(scan);
     if (e != cudaSuccess) return e;
     e = launch_behind(scan, dim3((unsigned)(N * HV * (D / kScanRows))), 128, bytes, s, cu, N, T, HV,
                       static_cast<uint8_t *>(ws), lay, status);

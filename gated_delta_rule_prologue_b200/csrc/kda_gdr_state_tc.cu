@@ -549,8 +549,7 @@ cudaError_t launch_typed(const void *v, const float *s0, const int32_t *cu, floa
                          int HK, int HV, kda_dtype dt, void *ws, float *o, float *sN, int *status,
                          cudaStream_t s) {
   auto kern = gdr_state_tc_kernel<Tin, kRole>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  const cudaError_t e = allow_smem<(int)kSmem>(kern);
   if (e != cudaSuccess) return e;
   const Layout lay = layout(N, T, HK, HV, D, kRole == kKeep);
   const long long units = lay.seg_chunks ? segment_slots(N, T, lay.seg_chunks) : N;
