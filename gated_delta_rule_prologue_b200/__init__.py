@@ -783,7 +783,9 @@ def kda_gdr_decode_step(q, k, v, g, beta, state, o, *, scale: float = 1.0, strea
 
 def kda_gdr_chunk_fwd_workspace_bytes(N: int, T: int, HK: int, HV: int, D: int,
                                       dtype: torch.dtype) -> int:
-    """Scratch bytes of :func:`kda_gdr_chunk_fwd` (0: it runs the recurrent form)."""
+    """Scratch bytes of the fastest form of :func:`kda_gdr_chunk_fwd` (0: it runs the recurrent
+    form).  They do not grow with N and T, but a workspace for the largest N and T serves every
+    smaller one, in the fastest form that fits."""
     return int(lib.kda_gdr_chunk_fwd_workspace_bytes(N, T, HK, HV, D, _DTYPES[dtype]))
 
 

@@ -1071,25 +1071,25 @@ kda_status kda_gdr_chunk_fwd_ws(const void *q, const void *k, const void *v, con
                                 const int32_t *cu_seqlens, int N, int T, int HK, int HV, int D,
                                 kda_dtype dt, float *o, float *final_state, void *workspace,
                                 size_t workspace_bytes, kda_stream_t stream) {
-  const size_t need = kda_gdr_chunk_fwd_workspace_bytes(N, T, HK, HV, D, dt);
-  if (workspace == nullptr || need == 0)
+  if (workspace == nullptr || !gdr_sizes_ok(N, T, HK, HV, D, dt))
     return kda_gdr_recurrent(q, k, v, g, beta, scale, initial_state, cu_seqlens, N, T, HK, HV, D,
                              dt, o, final_state, stream);
+  const kda::gdr::Layout lay = kda::gdr::layout(N, T, HK, HV, D, false, workspace_bytes);
   kda_status st = check_gdr_fwd(q, k, v, g, beta, initial_state, cu_seqlens, N, T, HK, HV, D, dt, o,
-                                final_state, workspace, need, "gdr_chunk_fwd");
+                                final_state, workspace, lay.bytes, "gdr_chunk_fwd");
   if (st != KDA_OK) return st;
   KDA_OPT_PTR(workspace, "workspace");
-  KDA_REQUIRE(workspace_bytes >= need, "workspace holds %zu bytes, these sizes need %zu",
-              workspace_bytes, need);
+  KDA_REQUIRE(workspace_bytes >= lay.bytes, "workspace holds %zu bytes, these sizes need %zu",
+              workspace_bytes, lay.bytes);
   int *status = nullptr;
   st = device_status_word(&status);
   if (st != KDA_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = kda::launch_gdr_prep(q, k, g, beta, cu_seqlens, N, T, HK, HV, D, dt, workspace,
-                                       false, status, s);
+                                       lay, status, s);
   if (e == cudaSuccess)
     e = kda::launch_gdr_state(v, initial_state, cu_seqlens, scale, N, T, HK, HV, D, dt, workspace,
-                              false, o, final_state, status, s);
+                              lay, false, o, final_state, status, s);
   if (e != cudaSuccess) return cuda_fail(e, "kda_gdr_chunk_fwd_ws launch");
   return KDA_OK;
 }
@@ -1122,7 +1122,8 @@ kda_status kda_gdr_chunk_bwd_ws(const void *q, const void *k, const void *v, con
   KDA_OPT_PTR(d_final_state, "d_final_state");
   KDA_OPT_PTR(d_initial_state, "d_initial_state");
   KDA_REQUIRE_PTR(workspace, "workspace");
-  const size_t need = kda::gdr::layout(N, T, HK, HV, D, true).bytes;
+  const kda::gdr::Layout lay = kda::gdr::layout(N, T, HK, HV, D, true);
+  const size_t need = lay.bytes;
   KDA_REQUIRE(workspace_bytes >= need, "workspace holds %zu bytes, these sizes need %zu",
               workspace_bytes, need);
   const size_t es = esize(dt), qk = (size_t)T * HK * D * es, vb = (size_t)T * HV * D * es;
@@ -1141,12 +1142,12 @@ kda_status kda_gdr_chunk_bwd_ws(const void *q, const void *k, const void *v, con
   if (st != KDA_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = kda::launch_gdr_prep(q, k, g, beta, cu_seqlens, N, T, HK, HV, D, dt, workspace,
-                                       true, status, s);
+                                       lay, status, s);
   if (e == cudaSuccess)
     e = kda::launch_gdr_state(v, initial_state, cu_seqlens, scale, N, T, HK, HV, D, dt, workspace,
-                              true, nullptr, nullptr, status, s);
+                              lay, true, nullptr, nullptr, status, s);
   if (e == cudaSuccess)
-    e = kda::launch_gdr_bwd(v, g, beta, cu_seqlens, scale, N, T, HK, HV, D, dt, workspace, d_o,
+    e = kda::launch_gdr_bwd(v, g, beta, cu_seqlens, scale, N, T, HK, HV, D, dt, workspace, lay, d_o,
                             d_final_state, dq, dk, dv, dg, dbeta, d_initial_state, status, s);
   if (e != cudaSuccess) return cuda_fail(e, "kda_gdr_chunk_bwd_ws launch");
   return KDA_OK;

@@ -65,8 +65,9 @@ __host__ __device__ inline long long segment_slots(int N, int T, int L) {
 // Chunks per segment (0: whole sequences), by a model of B200 measurements for sequences of about
 // T / N tokens, one CTA per (segment, head) and SM.  Microseconds for D = 128 (64): a chunk 4.9 (3.5)
 // of whole sequences, 4.2 (2.2) of a map, 5.3 (3.5) of a segment's read-out, a wave of either 3 more,
-// a step of the scan 2 (0.9), the two more launches 13 (4).  Cutting has to save a tenth.
-inline int segment_chunks(int N, int T, int HV, int D) {
+// a step of the scan 2 (0.9), the two more launches 13 (4).  Cutting has to save a tenth.  `room`: the
+// segments whose maps and states the workspace can hold (segment_slots times heads).
+inline int segment_chunks(int N, int T, int HV, int D, long long room) {
   const long long ctas = (long long)N * HV;
   if (N < 1 || T < 1 || ctas > 148) return 0;
   const bool d128 = D == 128;
@@ -77,7 +78,7 @@ inline int segment_chunks(int N, int T, int HV, int D) {
   int len = 0;
   for (long long G = 2; G <= n / 2 && G <= 64; ++G) {
     const long long L = (n + G - 1) / G, Gs = (n + L - 1) / L;
-    if (Gs < 2) continue;
+    if (Gs < 2 || segment_slots(N, T, (int)L) * HV > room) continue;
     const long long maps = ctas * (2 * Gs - 3), reads = ctas * Gs;
     const double t = (double)((maps + 147) / 148) * (L * map + 3.0) +
                      (double)((reads + 147) / 148) * (L * read + 3.0) + step * (double)(Gs - 2) + more;
@@ -111,7 +112,10 @@ struct Layout {
   size_t seg_m, seg_b, seg_e;    // and per segment M (map_bytes), fp32 B and first state, like a state
   size_t bytes;
 };
-inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
+// The layout that a workspace of `given` bytes has: the fastest of those that fit, down to the records
+// alone, whose bytes grow with N and T (what the fastest takes does not: few long sequences are cut, many
+// are not).  Without `given`, the fastest.  `bytes` says what it takes.
+inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd, size_t given = SIZE_MAX) {
   const size_t n = (size_t)slots(N, T);
   Layout l;
   l.kq = 0;
@@ -123,9 +127,11 @@ inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd) {
   l.x = l.u + (bwd ? rows : 0);
   l.scales = l.x + (bwd ? rows : 0);
   l.seg_m = l.scales + (bwd ? n * HV * 2 * (size_t)D * 4 : 0);
-  l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV, D);
+  const size_t seg1 = (size_t)D * D * 4;
+  const size_t room = given > l.seg_m ? (given - l.seg_m) / (map_bytes(D) + 2 * seg1) : 0;
+  l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV, D, (long long)room);
   const size_t segs = l.seg_chunks ? (size_t)segment_slots(N, T, l.seg_chunks) * HV : 0;
-  const size_t seg = segs * D * D * 4;
+  const size_t seg = segs * seg1;
   l.seg_b = l.seg_m + segs * map_bytes(D);
   l.seg_e = l.seg_b + seg;
   l.bytes = l.seg_e + seg;
@@ -435,18 +441,19 @@ __device__ __forceinline__ void load_rows_bt(uint32_t (&r)[4], uint32_t base, in
 }
 }  // namespace gdr
 
-// Host side (kda_gdr_*.cu), called by kda_api.cu; the *_tc form is launch_gdr_state's for D = 128.
+// Host side (kda_gdr_*.cu), called by kda_api.cu with one layout for all of a call; the *_tc form is launch_gdr_state's for D = 128.
 cudaError_t launch_gdr_state_tc(const void *v, const float *s0, const int32_t *cu, float scale, int N,
-                                int T, int HK, int HV, kda_dtype dt, void *ws, gdr::Role role,
-                                float *o, float *sN, int *status, cudaStream_t s);
+                                int T, int HK, int HV, kda_dtype dt, void *ws, const gdr::Layout &lay,
+                                gdr::Role role, float *o, float *sN, int *status, cudaStream_t s);
 cudaError_t launch_gdr_prep(const void *q, const void *k, const float *g, const float *beta,
                             const int32_t *cu, int N, int T, int HK, int HV, int D, kda_dtype dt,
-                            void *ws, bool bwd, int *status, cudaStream_t s);
+                            void *ws, const gdr::Layout &lay, int *status, cudaStream_t s);
 cudaError_t launch_gdr_state(const void *v, const float *s0, const int32_t *cu, float scale, int N,
-                             int T, int HK, int HV, int D, kda_dtype dt, void *ws, bool bwd, float *o,
-                             float *sN, int *status, cudaStream_t s);
+                             int T, int HK, int HV, int D, kda_dtype dt, void *ws,
+                             const gdr::Layout &lay, bool bwd, float *o, float *sN, int *status,
+                             cudaStream_t s);
 cudaError_t launch_gdr_bwd(const void *v, const float *g, const float *beta, const int32_t *cu,
                            float scale, int N, int T, int HK, int HV, int D, kda_dtype dt, void *ws,
-                           const float *d_o, const float *d_sN, void *dq, void *dk, void *dv,
+                           const gdr::Layout &lay, const float *d_o, const float *d_sN, void *dq, void *dk, void *dv,
                            float *dg, float *dbeta, float *d_s0, int *status, cudaStream_t s);
 }  // namespace kda

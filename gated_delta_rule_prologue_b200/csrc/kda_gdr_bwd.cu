@@ -1183,8 +1183,8 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
 
 template <typename Tin, int D>
 cudaError_t launch_reverse(const int32_t *cu, float scale, int N, int T, int HK, int HV, void *ws,
-                           const float *d_o, const float *d_sN, void *dv, float *d_s0, int *status,
-                           cudaStream_t s) {
+                           const Layout &lay, const float *d_o, const float *d_sN, void *dv, float *d_s0,
+                           int *status, cudaStream_t s) {
   // Two CTAs of 64 value channels per head as long as all of them run at once (5.6 us a chunk), else whole
   // heads (10.4 us; the two halves on one SM in turn 11.2), as the forward (kda_gdr_state.cu).
   const bool whole = D == 128 && (long long)N * HV * 2 > 148;
@@ -1204,16 +1204,16 @@ cudaError_t launch_reverse(const int32_t *cu, float scale, int N, int T, int HK,
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
   if (e != cudaSuccess) return e;
   return launch_behind(kern, dim3((unsigned)ctas), 256, bytes, s, d_o, d_sN, cu, scale, N, T, HK, HV,
-                       static_cast<uint8_t *>(ws), layout(N, T, HK, HV, D, true), static_cast<Tin *>(dv),
+                       static_cast<uint8_t *>(ws), lay, static_cast<Tin *>(dv),
                        d_s0, status);
 }
 
 template <typename Tin, int D>
 cudaError_t launch_typed(const void *v, const float *g, const float *beta, const int32_t *cu,
-                         float scale, int N, int T, int HK, int HV, void *ws, const float *d_o,
-                         const float *d_sN, void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                         float scale, int N, int T, int HK, int HV, void *ws, const Layout &lay,
+                         const float *d_o, const float *d_sN, void *dq, void *dk, void *dv, float *dg, float *dbeta,
                          float *d_s0, int *status, cudaStream_t s) {
-  cudaError_t e = launch_reverse<Tin, D>(cu, scale, N, T, HK, HV, ws, d_o, d_sN, dv, d_s0, status, s);
+  cudaError_t e = launch_reverse<Tin, D>(cu, scale, N, T, HK, HV, ws, lay, d_o, d_sN, dv, d_s0, status, s);
   if (e != cudaSuccess) return e;
   auto kern = gdr_local_kernel<Tin, D>;
   constexpr int bytes = (int)LocalSmem<D>::kBytes;
@@ -1223,7 +1223,7 @@ cudaError_t launch_typed(const void *v, const float *g, const float *beta, const
   const unsigned ctas = (unsigned)(items < 148 ? items : 148);  // one per SM
   kern<<<ctas, kLocalThreads, bytes, s>>>(
       static_cast<const Tin *>(v), g, beta, d_o, cu, scale, N, T, HK, HV,
-      static_cast<const uint8_t *>(ws), layout(N, T, HK, HV, D, true), static_cast<Tin *>(dq),
+      static_cast<const uint8_t *>(ws), lay, static_cast<Tin *>(dq),
       static_cast<Tin *>(dk), dg, dbeta, status);
   return cudaGetLastError();
 }
@@ -1232,15 +1232,15 @@ cudaError_t launch_typed(const void *v, const float *g, const float *beta, const
 
 cudaError_t launch_gdr_bwd(const void *v, const float *g, const float *beta, const int32_t *cu,
                            float scale, int N, int T, int HK, int HV, int D, kda_dtype dt, void *ws,
-                           const float *d_o, const float *d_sN, void *dq, void *dk, void *dv,
+                           const Layout &lay, const float *d_o, const float *d_sN, void *dq, void *dk, void *dv,
                            float *dg, float *dbeta, float *d_s0, int *status, cudaStream_t s) {
   const bool bf = dt == KDA_BF16;
   if (D == 128)
-    return bf ? launch_typed<__nv_bfloat16, 128>(v, g, beta, cu, scale, N, T, HK, HV, ws, d_o, d_sN, dq, dk, dv, dg, dbeta, d_s0, status, s)
-              : launch_typed<__half, 128>(v, g, beta, cu, scale, N, T, HK, HV, ws, d_o, d_sN, dq, dk, dv, dg, dbeta, d_s0, status, s);
+    return bf ? launch_typed<__nv_bfloat16, 128>(v, g, beta, cu, scale, N, T, HK, HV, ws, lay, d_o, d_sN, dq, dk, dv, dg, dbeta, d_s0, status, s)
+              : launch_typed<__half, 128>(v, g, beta, cu, scale, N, T, HK, HV, ws, lay, d_o, d_sN, dq, dk, dv, dg, dbeta, d_s0, status, s);
   if (D == 64)
-    return bf ? launch_typed<__nv_bfloat16, 64>(v, g, beta, cu, scale, N, T, HK, HV, ws, d_o, d_sN, dq, dk, dv, dg, dbeta, d_s0, status, s)
-              : launch_typed<__half, 64>(v, g, beta, cu, scale, N, T, HK, HV, ws, d_o, d_sN, dq, dk, dv, dg, dbeta, d_s0, status, s);
+    return bf ? launch_typed<__nv_bfloat16, 64>(v, g, beta, cu, scale, N, T, HK, HV, ws, lay, d_o, d_sN, dq, dk, dv, dg, dbeta, d_s0, status, s)
+              : launch_typed<__half, 64>(v, g, beta, cu, scale, N, T, HK, HV, ws, lay, d_o, d_sN, dq, dk, dv, dg, dbeta, d_s0, status, s);
   return cudaErrorInvalidValue;
 }
 

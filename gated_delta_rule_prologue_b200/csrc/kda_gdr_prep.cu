@@ -414,8 +414,8 @@ gdr_prep_kernel(const Tin *__restrict__ q, const Tin *__restrict__ k, const floa
 
 template <typename Tin, int D>
 cudaError_t launch_typed(const void *q, const void *k, const float *g, const float *beta,
-                         const int32_t *cu, int N, int T, int HK, int HV, void *ws, bool bwd,
-                         int *status, cudaStream_t s) {
+                         const int32_t *cu, int N, int T, int HK, int HV, void *ws,
+                         const Layout &lay, int *status, cudaStream_t s) {
   auto kern = gdr_prep_kernel<Tin, D>;
   constexpr int bytes = (int)sizeof(PrepSmem<D>);
   const cudaError_t e = allow_smem<bytes>(kern);
@@ -424,7 +424,7 @@ cudaError_t launch_typed(const void *q, const void *k, const float *g, const flo
   if (ctas >= (1LL << 31)) return cudaErrorInvalidValue;
   kern<<<(unsigned)ctas, kThreads, bytes, s>>>(
       static_cast<const Tin *>(q), static_cast<const Tin *>(k), g, beta, cu, N, T, HK, HV,
-      static_cast<uint8_t *>(ws), layout(N, T, HK, HV, D, bwd), status);
+      static_cast<uint8_t *>(ws), lay, status);
   return cudaGetLastError();
 }
 
@@ -432,14 +432,14 @@ cudaError_t launch_typed(const void *q, const void *k, const float *g, const flo
 
 cudaError_t launch_gdr_prep(const void *q, const void *k, const float *g, const float *beta,
                             const int32_t *cu, int N, int T, int HK, int HV, int D, kda_dtype dt,
-                            void *ws, bool bwd, int *status, cudaStream_t s) {
+                            void *ws, const Layout &lay, int *status, cudaStream_t s) {
   const bool bf = dt == KDA_BF16;
   if (D == 128)
-    return bf ? launch_typed<__nv_bfloat16, 128>(q, k, g, beta, cu, N, T, HK, HV, ws, bwd, status, s)
-              : launch_typed<__half, 128>(q, k, g, beta, cu, N, T, HK, HV, ws, bwd, status, s);
+    return bf ? launch_typed<__nv_bfloat16, 128>(q, k, g, beta, cu, N, T, HK, HV, ws, lay, status, s)
+              : launch_typed<__half, 128>(q, k, g, beta, cu, N, T, HK, HV, ws, lay, status, s);
   if (D == 64)
-    return bf ? launch_typed<__nv_bfloat16, 64>(q, k, g, beta, cu, N, T, HK, HV, ws, bwd, status, s)
-              : launch_typed<__half, 64>(q, k, g, beta, cu, N, T, HK, HV, ws, bwd, status, s);
+    return bf ? launch_typed<__nv_bfloat16, 64>(q, k, g, beta, cu, N, T, HK, HV, ws, lay, status, s)
+              : launch_typed<__half, 64>(q, k, g, beta, cu, N, T, HK, HV, ws, lay, status, s);
   return cudaErrorInvalidValue;
 }
 

@@ -502,9 +502,8 @@ cudaError_t launch_role(const void *v, const float *s0, const int32_t *cu, float
 
 template <typename Tin, int D>
 cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float scale, int N, int T,
-                     int HK, int HV, void *ws, bool bwd, float *o, float *sN, int *status,
-                     cudaStream_t s) {
-  const Layout lay = layout(N, T, HK, HV, D, bwd);
+                     int HK, int HV, void *ws, const Layout &lay, bool bwd, float *o, float *sN,
+                     int *status, cudaStream_t s) {
   // D = 128: two CTAs of four warps per head, one per SM, if they all run at once, or else, and for
   // segments, which fill the SMs by themselves, the tcgen05 form with one CTA per head.  Microseconds a
   // chunk, here and there: with the read-out 4.9 and 5.3, kept for the backward 3.9 and 6.3, maps 4.1 and 4.2.
@@ -512,12 +511,12 @@ cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float sc
   const kda_dtype dt = std::is_same<Tin, __half>::value ? KDA_F16 : KDA_BF16;
   if (bwd)
     return tensor_memory
-               ? launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, kKeep, o, sN, status, s)
+               ? launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, lay, kKeep, o, sN, status, s)
                : launch_role<Tin, D, 4, kKeep>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
   if (lay.seg_chunks) {
     cudaError_t e;
     if constexpr (D == 128)
-      e = launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, kMap, o, sN, status, s);
+      e = launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, lay, kMap, o, sN, status, s);
     else
       e = launch_role<Tin, D, 4, kMap>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
     if (e != cudaSuccess) return e;
@@ -530,20 +529,20 @@ cudaError_t launch_d(const void *v, const float *s0, const int32_t *cu, float sc
     if (e != cudaSuccess) return e;
   }
   return tensor_memory
-             ? launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, kOut, o, sN, status, s)
+             ? launch_gdr_state_tc(v, s0, cu, scale, N, T, HK, HV, dt, ws, lay, kOut, o, sN, status, s)
              : launch_role<Tin, D, 4, kOut>(v, s0, cu, scale, N, T, HK, HV, ws, lay, o, sN, status, s);
 }
 
 }  // namespace
 
 cudaError_t launch_gdr_state(const void *v, const float *s0, const int32_t *cu, float scale, int N,
-                             int T, int HK, int HV, int D, kda_dtype dt, void *ws, bool bwd, float *o,
-                             float *sN, int *status, cudaStream_t s) {
+                             int T, int HK, int HV, int D, kda_dtype dt, void *ws, const Layout &lay,
+                             bool bwd, float *o, float *sN, int *status, cudaStream_t s) {
   if (dt == KDA_BF16)
-    return D == 64 ? launch_d<__nv_bfloat16, 64>(v, s0, cu, scale, N, T, HK, HV, ws, bwd, o, sN, status, s)
-                   : launch_d<__nv_bfloat16, 128>(v, s0, cu, scale, N, T, HK, HV, ws, bwd, o, sN, status, s);
-  return D == 64 ? launch_d<__half, 64>(v, s0, cu, scale, N, T, HK, HV, ws, bwd, o, sN, status, s)
-                 : launch_d<__half, 128>(v, s0, cu, scale, N, T, HK, HV, ws, bwd, o, sN, status, s);
+    return D == 64 ? launch_d<__nv_bfloat16, 64>(v, s0, cu, scale, N, T, HK, HV, ws, lay, bwd, o, sN, status, s)
+                   : launch_d<__nv_bfloat16, 128>(v, s0, cu, scale, N, T, HK, HV, ws, lay, bwd, o, sN, status, s);
+  return D == 64 ? launch_d<__half, 64>(v, s0, cu, scale, N, T, HK, HV, ws, lay, bwd, o, sN, status, s)
+                 : launch_d<__half, 128>(v, s0, cu, scale, N, T, HK, HV, ws, lay, bwd, o, sN, status, s);
 }
 
 }  // namespace kda

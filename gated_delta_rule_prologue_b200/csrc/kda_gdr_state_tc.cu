@@ -546,12 +546,11 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
 
 template <typename Tin, int kRole>
 cudaError_t launch_typed(const void *v, const float *s0, const int32_t *cu, float scale, int N, int T,
-                         int HK, int HV, kda_dtype dt, void *ws, float *o, float *sN, int *status,
-                         cudaStream_t s) {
+                         int HK, int HV, kda_dtype dt, void *ws, const Layout &lay, float *o, float *sN,
+                         int *status, cudaStream_t s) {
   auto kern = gdr_state_tc_kernel<Tin, kRole>;
   const cudaError_t e = allow_smem<(int)kSmem>(kern);
   if (e != cudaSuccess) return e;
-  const Layout lay = layout(N, T, HK, HV, D, kRole == kKeep);
   const long long units = lay.seg_chunks ? segment_slots(N, T, lay.seg_chunks) : N;
   const long long ctas = units * HV * (kRole == kMap ? 2 : 1);
   CUtensorMap tm;
@@ -560,7 +559,7 @@ cudaError_t launch_typed(const void *v, const float *s0, const int32_t *cu, floa
                        static_cast<uint8_t *>(ws), lay, o, sN, status);
 }
 
-template <typename Tin, typename... Args> cudaError_t launch_for(Role role, Args... args) {
+template <typename Tin, typename... Args> cudaError_t launch_for(Role role, const Args &...args) {
   return role == kOut    ? launch_typed<Tin, kOut>(args...)
          : role == kKeep ? launch_typed<Tin, kKeep>(args...)
                          : launch_typed<Tin, kMap>(args...);
@@ -569,11 +568,11 @@ template <typename Tin, typename... Args> cudaError_t launch_for(Role role, Args
 }  // namespace
 
 cudaError_t launch_gdr_state_tc(const void *v, const float *s0, const int32_t *cu, float scale, int N,
-                                int T, int HK, int HV, kda_dtype dt, void *ws, Role role, float *o,
-                                float *sN, int *status, cudaStream_t s) {
+                                int T, int HK, int HV, kda_dtype dt, void *ws, const Layout &lay, Role role,
+                                float *o, float *sN, int *status, cudaStream_t s) {
   return dt == KDA_BF16
-             ? launch_for<__nv_bfloat16>(role, v, s0, cu, scale, N, T, HK, HV, dt, ws, o, sN, status, s)
-             : launch_for<__half>(role, v, s0, cu, scale, N, T, HK, HV, dt, ws, o, sN, status, s);
+             ? launch_for<__nv_bfloat16>(role, v, s0, cu, scale, N, T, HK, HV, dt, ws, lay, o, sN, status, s)
+             : launch_for<__half>(role, v, s0, cu, scale, N, T, HK, HV, dt, ws, lay, o, sN, status, s);
 }
 
 }  // namespace kda

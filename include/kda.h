@@ -582,10 +582,16 @@ kda_status kda_gdr_decode_step(const void *q, const void *k, const void *v, cons
  * kda_gdr_chunk_fwd_ws -- the prefill in chunks of 64 tokens: a prep pass over all
  * chunks (decay matrix, Gram products, the inverse of the unit lower triangular
  * system), then a state pass over the chunks of each sequence in order.
- *   workspace        >= kda_gdr_chunk_fwd_workspace_bytes(...) bytes, 16-byte
+ *   workspace        kda_gdr_chunk_fwd_workspace_bytes(...) bytes, 16-byte
  *                    aligned, caller-owned; contents on entry do not matter.  Calls
  *                    that may run at the same time must not share one.  NULL runs
  *                    kda_gdr_recurrent.
+ * The size function gives what the fastest form takes, which is more for few long
+ * sequences than for many: it does not grow with N and T.  What a call cannot do
+ * without does, and a call with less than the fastest form's takes the fastest that
+ * fits (KDA_ERR_INVALID_ARG if none does).  So a workspace of the size for the largest
+ * N and T serves every smaller one.  The form, and with it the last bits of the
+ * results, depends on the sizes and on workspace_bytes alone.
  * The chunked form is for dt KDA_BF16 or KDA_F16 and D 64 or 128; for other types
  * and sizes (kda_gdr_chunk_fwd_workspace_bytes is 0 then) the call is
  * kda_gdr_recurrent.  Products run on the tensor cores on fp16 terms: q and k

@@ -206,3 +206,13 @@ def test_binding_refuses_cpu_tensors(kda):
         kda.kda_gdr_chunk_fwd(q[0], q[0], q[0], q, q, q)
     with pytest.raises(ValueError, match="CUDA"):
         kda.kda_output_epilogue_bwd(q, q, q[0, 0], q, q, q)
+
+
+def test_chunk_forward_refuses_less_than_the_records(kda):
+    """Few long sequences: the size that is asked for holds segments beside the records, and what is
+    refused is what does not hold the records."""
+    f = kda.lib.kda_gdr_chunk_fwd_workspace_bytes
+    records = f(1000, 4000, 1, 2, 128, 1) - 999 * (f(1001, 4000, 1, 2, 128, 1) - f(1000, 4000, 1, 2, 128, 1))
+    assert f(1, 4000, 1, 2, 128, 1) > records
+    refused(kda, gdr(kda, "kda_gdr_chunk_fwd_ws", N=1, T=4000, HK=1, HV=2, nbytes=records - 1), 1,
+            b"workspace holds %d bytes, these sizes need %d" % (records - 1, records))
