@@ -14,9 +14,12 @@
 // Arithmetic.  Products run on the tensor cores with fp32 sums.  The keys and queries are exact
 // in fp16 (one power of two per 64-token tile keeps bf16 inputs of any size in range); every
 // other operand (state, U, T, P, gradients) is split in two fp16 terms, x 2^-e = hi + lo, with a
-// power of two per row that puts the row's largest value in [1, 2): 22 significant bits, so
-// results carry fp32-like errors and no value of the fp32 range overflows.  A product of a split
-// operand with an exact one takes two MMAs, of two split ones three (hi hi, hi lo, lo hi).
+// power of two per row that puts the row's largest value in [1, 2): 22 significant bits below that,
+// so a product's errors are those of fp32 arithmetic on rows whose values are all as large as their
+// largest, and no value of the fp32 range overflows.  Rows are, in the state passes, a value channel over
+// the key channels or over the chunk's 64 tokens; in the local pass a token over the channels (dO, X, U)
+// or over the chunk's tokens (W, M), and a key channel over the value channels (S, dS').  A product of a
+// split operand with an exact one takes two MMAs, of two split ones three (hi hi, hi lo, lo hi).
 //
 // Workspace: records of the chunks.  Chunk c of sequence n, whose first token is bos, has slot
 // bos / 64 + n + c (strictly increasing from chunk to chunk, so no index pass is needed; T / 64 +
@@ -107,7 +110,6 @@ struct Layout {
   size_t kq, tp;                 // records
   size_t state, dstate, u, x;    // backward: per chunk fp32 S and dS' (key-major: [key][value channel]),
                                  // U and X [64][D]
-  size_t scales;                 // backward: per chunk the scales of the value channels of S, then of dS'
   int seg_chunks;                // forward: chunks per segment, or 0
   size_t seg_m, seg_b, seg_e;    // and per segment M (map_bytes), fp32 B and first state, like a state
   size_t bytes;
@@ -125,8 +127,7 @@ inline Layout layout(int N, int T, int HK, int HV, int D, bool bwd, size_t given
   l.dstate = l.state + (bwd ? sq : 0);
   l.u = l.dstate + (bwd ? sq : 0);
   l.x = l.u + (bwd ? rows : 0);
-  l.scales = l.x + (bwd ? rows : 0);
-  l.seg_m = l.scales + (bwd ? n * HV * 2 * (size_t)D * 4 : 0);
+  l.seg_m = l.x + (bwd ? rows : 0);
   const size_t seg1 = (size_t)D * D * 4;
   const size_t room = given > l.seg_m ? (given - l.seg_m) / (map_bytes(D) + 2 * seg1) : 0;
   l.seg_chunks = bwd ? 0 : segment_chunks(N, T, HV, D, (long long)room);

@@ -128,11 +128,6 @@ gdr_reverse_kernel(const float *__restrict__ d_o, const float *d_sN, const int32
     zero(du);
     Scale a0, a1;
     row_scales(s, a0, a1);
-    if ((lane & 3) == 0) {
-      float *p = reinterpret_cast<float *>(ws + lay.scales) + rec * 2 * D + D + row;
-      p[0] = a0.s;
-      p[8] = a1.s;
-    }
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       uint32_t hi[4], lo[4];
@@ -493,11 +488,6 @@ gdr_reverse_pair_kernel(const float *__restrict__ d_o, const float *d_sN, const 
     zero(du);
     Scale a0, a1, r0, r1;
     row_scales(s, a0, a1);
-    if ((lane & 3) == 0) {
-      float *p = reinterpret_cast<float *>(ws + lay.scales) + rec * 2 * D + D + row;
-      p[0] = a0.s;
-      p[8] = a1.s;
-    }
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       uint32_t hi[4], lo[4];
@@ -598,6 +588,11 @@ gdr_reverse_pair_kernel(const float *__restrict__ d_o, const float *d_sN, const 
 
 constexpr int kLocalThreads = 256;
 
+__device__ __forceinline__ uint32_t times2(uint32_t x, __half2 f) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x), f);
+  return *reinterpret_cast<const uint32_t *>(&y);
+}
+
 template <int D> struct LocalSmem {
   static constexpr uint32_t kK = 0, kQ = kQRows;
   static constexpr uint32_t kS = kq_tile_bytes(D);   // S, D rows (key channels)
@@ -611,39 +606,32 @@ template <int D> struct LocalSmem {
     float cols[4][C];                  // per row block: column sums
     float tail[2][C], zk[2][C], db[2][C];
     float cross[8];
+    float row_max[2][2][C];            // of W and M, per half
+    float most[8][2];                  // and per warp
+    float scale[2][C + 1];             // of W's and M's rows, and the largest
+    alignas(4) __half rel[2][C];       // the rows' over the largest
   };
+  static_assert(sizeof(Sums) <= C * D * 4, "the sums fit where X was");
   struct Small {
-    alignas(16) float scales[2][D];      // of the value channels of S and of dS', as the passes left them
+    alignas(16) float scales[2][D];      // of the rows (key channels) of S and of dS'
     alignas(16) float2 gamma[C];
     float beta[C], us[C], as[C], xv[C];  // us, as: scales of U's and of dO's or X's rows
-    float red[8][2];
     alignas(16) float kq[4];             // the tile's two scales
     uint64_t states, rest;               // S and dS' have landed; U (and K and Q) have
   };
   static constexpr uint32_t kBytes = kSmall + sizeof(Small);
 };
 
-// The largest over the block of each of two values (one barrier pair).
-__device__ __forceinline__ float2 block_max2(float a, float b, float (*red)[2]) {
+// One step of a reduction that folds 2 n values a lane to n: a lane keeps the lower or the upper half, by
+// its bit `off`, each the larger of its own and the other lane's.
+template <int n> __device__ __forceinline__ void fold_max(float *x, int off) {
+  const bool upper = threadIdx.x & off;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-    b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
+  for (int i = 0; i < n; ++i) {
+    const float other = __shfl_xor_sync(0xffffffffu, upper ? x[i] : x[i + n], off);
+    x[i] = fmaxf(upper ? x[i + n] : x[i], other);
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
-    red[threadIdx.x >> 5][0] = a;
-    red[threadIdx.x >> 5][1] = b;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a = fmaxf(a, red[i][0]);
-    b = fmaxf(b, red[i][1]);
-  }
-  return make_float2(a, b);
 }
-
 __device__ __forceinline__ float max_abs4(const float4 &x, float m) {
   return fmaxf(fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
 }
@@ -663,11 +651,12 @@ __device__ __forceinline__ float2 tile_pair(const uint8_t *tile, int row, int c8
 
 // Persistent: a CTA takes every gridDim.x-th (chunk, key head).  S and dS' of the next (chunk,
 // head) are fetched as soon as this one's have been used, behind the products that are left.
-// A warp splits its rows of S and of dS' in their places (row_off; whole rows, so no block barrier), and
-// sums their products on the way.  `rows` is a multiple of four accesses of 128 / D rows.
+// A warp splits its rows of S and of dS' in their places (row_off; whole rows, so no block barrier), each
+// row with its own power of two, and sums their products on the way.  `rows` is a multiple of four accesses
+// of 128 / D rows.
 template <int D>
-__device__ __forceinline__ float split_states_in_place(uint8_t *s, uint8_t *ds, int row0, int rows, float inv,
-                                                       float dinv) {
+__device__ __forceinline__ float split_states_in_place(uint8_t *s, uint8_t *ds, int row0, int rows,
+                                                       float (*scales)[D]) {
   constexpr int LR = D / 4, RP = 32 / LR;  // lanes per row, rows per warp access
   const int lane = threadIdx.x & 31, rl = lane / LR, cl = lane % LR;
   float cross = 0.f;
@@ -680,6 +669,20 @@ __device__ __forceinline__ float split_states_in_place(uint8_t *s, uint8_t *ds, 
       x[0][k] = *reinterpret_cast<const float4 *>(s + at);
       x[1][k] = *reinterpret_cast<const float4 *>(ds + at);
     }
+    // The rows' largest: folded to one row of one matrix per lane, and exchanged.
+    float big[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) big[k] = max_abs4(x[k >> 2][k & 3], 0.f);
+    fold_max<4>(big, LR / 2);
+    fold_max<2>(big, LR / 4);
+    fold_max<1>(big, LR / 8);
+#pragma unroll
+    for (int off = LR / 16; off > 0; off >>= 1) big[0] = fmaxf(big[0], __shfl_xor_sync(0xffffffffu, big[0], off));
+    const Scale mine = scale_of(big[0]);
+    if (cl % (LR / 8) == 0) {
+      const int j = cl / (LR / 8);
+      scales[j >> 2][row0 + i + (j & 3) * RP + rl] = mine.s;
+    }
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -689,10 +692,11 @@ __device__ __forceinline__ float split_states_in_place(uint8_t *s, uint8_t *ds, 
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const float4 &y = x[which][k];
+        const float inv = __shfl_sync(0xffffffffu, mine.inv, rl * LR + (4 * which + k) * (LR / 8));
         uint8_t *to = (which ? ds : s) + o;
         uint2 hi, lo;
-        split2(y.x, y.y, which ? dinv : inv, hi.x, lo.x);
-        split2(y.z, y.w, which ? dinv : inv, hi.y, lo.y);
+        split2(y.x, y.y, inv, hi.x, lo.x);
+        split2(y.z, y.w, inv, hi.y, lo.y);
         *reinterpret_cast<uint2 *>(to) = hi;
         *reinterpret_cast<uint2 *>(to + 2 * D) = lo;
       }
@@ -738,10 +742,9 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
   // One thread: S and dS' of a (chunk, head), 4 D^2 bytes each as the state passes left them.
   auto fetch_states = [&](long long item, int j) {
     const size_t rec = (size_t)(item / HK) * HV + item % HK * group + j;
-    tc::mbar_arrive_expect_tx(&sm.states, 2 * D * D * 4 + 2 * D * 4);
+    tc::mbar_arrive_expect_tx(&sm.states, 2 * D * D * 4);
     tc::bulk_load(smem + Sm::kS, ws + lay.state + rec * D * D * 4, D * D * 4, &sm.states);
     tc::bulk_load(smem + Sm::kD, ws + lay.dstate + rec * D * D * 4, D * D * 4, &sm.states);
-    tc::bulk_load(sm.scales, ws + lay.scales + rec * 2 * D * 4, 2 * D * 4, &sm.states);
   };
   // A warp's 8 of 64 rows, held in registers, with a scale per row.
   constexpr int kHeld = 8 / RP;
@@ -831,7 +834,7 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
         sm.beta[lane] = small[0];
         sm.beta[lane + 32] = small[1];
       }
-      // S and dS' with one power of two per matrix, and <dS', S>.
+      // S and dS', a power of two per key channel, and <dS', S>.
       if (!tc::wait_all(&sm.states, par, status)) {
         if (tid == 0) {  // what is in flight lands before the CTA's memory goes
           tc::drain(&sm.states);
@@ -841,19 +844,8 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
         __syncthreads();
         return;
       }
-      float2 big = make_float2(0.f, 0.f);
-      if (lane < D / 4) {
-        big.x = max_abs4(reinterpret_cast<const float4 *>(sm.scales[0])[lane], 0.f);
-        big.y = max_abs4(reinterpret_cast<const float4 *>(sm.scales[1])[lane], 0.f);
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        big.x = fmaxf(big.x, __shfl_xor_sync(0xffffffffu, big.x, off));
-        big.y = fmaxf(big.y, __shfl_xor_sync(0xffffffffu, big.y, off));
-      }
-      const Scale ss = scale_of(big.x), ds = scale_of(big.y);
       constexpr int kRows = D / 8;  // of each matrix per warp
-      float cross = split_states_in_place<D>(smem + Sm::kS, smem + Sm::kD, kRows * warp, kRows, ss.inv, ds.inv);
+      float cross = split_states_in_place<D>(smem + Sm::kS, smem + Sm::kD, kRows * warp, kRows, sm.scales);
       cp_wait<0>();  // this thread's part of its own warp's rows of dO
       __syncwarp();
       split_own(Sm::kA, sm.as);
@@ -925,6 +917,15 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
           y[i][2] *= f1 * u.x; y[i][3] *= f1 * u.y;
         }
       };
+      // z's rows times f0, f1 and its columns times their key channels' scales.
+      auto scale_z = [&](float (&z)[NH][4], int which, float f0, float f1) {
+#pragma unroll
+        for (int i = 0; i < NH; ++i) {
+          const float2 s = *reinterpret_cast<const float2 *>(sm.scales[which] + half * (D / 2) + 8 * i + col);
+          z[i][0] *= f0 * s.x; z[i][1] *= f0 * s.y;
+          z[i][2] *= f1 * s.x; z[i][3] *= f1 * s.y;
+        }
+      };
       // Row dots of z with the rows of a tile (keys or queries), summed over this warp's columns.
       auto row_dots = [&](const float (&z)[NH][4], uint32_t tile, float f, float &d0, float &d1) {
         d0 = d1 = 0.f;
@@ -947,13 +948,11 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
         rows_times(Sm::kA, Sm::kS, z, dp, true);
         const float f0 = scale * sm.as[r0], f1 = scale * sm.as[r1];
         scale_y(dp, f0, f1);
-        const float z0 = g0 * f0 * ss.s, z1 = g1 * f1 * ss.s;
+        scale_z(z, 0, g0 * f0, g1 * f1);
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
-          z[i][0] *= z0; z[i][1] *= z0; z[i][2] *= z1; z[i][3] *= z1;
+        for (int i = 0; i < NH; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) aq[i][e] += z[i][e];
-        }
         row_dots(z, Sm::kQ, qs, rg0, rg1);
       }
       __syncthreads();
@@ -974,11 +973,7 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
         rows_times(Sm::kA, Sm::kS, z, da, true);
         const float f0 = sm.as[r0], f1 = sm.as[r1];
         scale_y(da, f0, f1);
-        const float z0 = f0 * ss.s, z1 = f1 * ss.s;
-#pragma unroll
-        for (int i = 0; i < NH; ++i) {
-          z[i][0] *= z0; z[i][1] *= z0; z[i][2] *= z1; z[i][3] *= z1;
-        }
+        scale_z(z, 0, f0, f1);
         row_dots(z, Sm::kK, ks, zk0, zk1);
         const float k0 = g0 * b0, k1 = g1 * b1;
         rg0 -= k0 * zk0;
@@ -992,20 +987,17 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
       {  // E U dS'^T
         rows_times(Sm::kU, Sm::kD, z, da, false);
         const float2 gl = sm.gamma[C - 1];
-        const float f0 = sm.us[r0] * ds.s * decay_between(gl, gr[0]);
-        const float f1 = sm.us[r1] * ds.s * decay_between(gl, gr[1]);
+        scale_z(z, 1, sm.us[r0] * decay_between(gl, gr[0]), sm.us[r1] * decay_between(gl, gr[1]));
 #pragma unroll
-        for (int i = 0; i < NH; ++i) {
-          z[i][0] *= f0; z[i][1] *= f0; z[i][2] *= f1; z[i][3] *= f1;
+        for (int i = 0; i < NH; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) ak[i][e] += z[i][e];
-        }
         row_dots(z, Sm::kK, ks, tl0, tl1);
       }
       // W, M and their sums over rows and columns; Q K^T and K K^T again, from the tiles.  A token's
       // own term decays by nothing: it stays out of the sums, where it would be added and taken
       // away again, next to which the others may be small.
-      float bigw = 0.f, bigm = 0.f, cs[4][2], nb[2] = {0.f, 0.f};
+      float row_w[2] = {0.f, 0.f}, row_m[2] = {0.f, 0.f}, cs[4][2], nb[2] = {0.f, 0.f};
       {
         float qk[4][4], kk2[4][4];
         zero(qk);
@@ -1044,8 +1036,8 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
             cs[i][e & 1] += t;
             dp[i][e] = w;
             da[i][e] = b * m0;
-            bigw = fmaxf(bigw, fabsf(w));
-            bigm = fmaxf(bigm, fabsf(da[i][e]));
+            row_w[e >> 1] = fmaxf(row_w[e >> 1], fabsf(w));
+            row_m[e >> 1] = fmaxf(row_m[e >> 1], fabsf(da[i][e]));
           }
           cs[i][0] = col_sum(cs[i][0]);
           cs[i][1] = col_sum(cs[i][1]);
@@ -1057,8 +1049,28 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
       }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) cross += __shfl_xor_sync(0xffffffffu, cross, off);
+      float most[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        row_w[e] = quad_max(row_w[e]);
+        row_m[e] = quad_max(row_m[e]);
+      }
+      most[0] = fmaxf(row_w[0], row_w[1]);
+      most[1] = fmaxf(row_m[0], row_m[1]);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        most[0] = fmaxf(most[0], __shfl_xor_sync(0xffffffffu, most[0], off));
+        most[1] = fmaxf(most[1], __shfl_xor_sync(0xffffffffu, most[1], off));
+      }
       tc::fence_async_smem();  // the split rows were ordinary writes; the copies below are not
-      const float2 most = block_max2(bigw, bigm, sm.red);  // also: S, dS', U, X have been read
+      __syncthreads();         // S, dS', U, X have been read
+      if (lane < 2) sums.most[warp][lane] = lane ? most[1] : most[0];
+      if ((lane & 3) == 0) {
+        sums.row_max[0][half][r0] = row_w[0];
+        sums.row_max[0][half][r1] = row_w[1];
+        sums.row_max[1][half][r0] = row_m[0];
+        sums.row_max[1][half][r1] = row_m[1];
+      }
       if (j + 1 < group) {
         if (tid == 0) fetch_states(item, j + 1);
         fetch_small(t0, len, h + 1);
@@ -1068,21 +1080,47 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
         if (following < items)
           fetch_small(bos + c * C, min(C, eos - bos - c * C), (int)(following % HK) * group);
       }
-      const Scale sw = scale_of(most.x), sn = scale_of(most.y);
+      __syncthreads();
+      // W and M, a power of two per row: a token's W K and M K are as exact for themselves where other
+      // tokens' rows are larger by many powers of two.  In W^T Q and M^T K, where the rows are summed
+      // over, they go to the operand as fp16 factors, exact down to 2^-24 of the largest row's value.
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int which = 0; which < 2; ++which) {
+        float(&y)[4][4] = which ? da : dp;
+        Scale s[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint32_t at = tile_off(e ? r1 : r0, 4 * half + i) + 2 * col;
-          uint32_t hi, lo;
-          split2(dp[i][2 * e], dp[i][2 * e + 1], sw.inv, hi, lo);
-          *reinterpret_cast<uint32_t *>(smem + Sm::kU + at) = hi;
-          *reinterpret_cast<uint32_t *>(smem + Sm::kU + kTriBytes + at) = lo;
-          split2(da[i][2 * e], da[i][2 * e + 1], sn.inv, hi, lo);
-          *reinterpret_cast<uint32_t *>(smem + Sm::kU + 2 * kTriBytes + at) = hi;
-          *reinterpret_cast<uint32_t *>(smem + Sm::kU + 3 * kTriBytes + at) = lo;
-          if (lane < 4) sums.cols[m][32 * half + 8 * i + col + e] = cs[i][e];
+          s[e] = scale_of(fmaxf(sums.row_max[which][0][e ? r1 : r0], sums.row_max[which][1][e ? r1 : r0]));
         }
+        float all = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all = fmaxf(all, sums.most[i][which]);
+        const Scale sa = scale_of(all);
+        if (tid == 0) sums.scale[which][C] = sa.s;
+        if (half == 0 && (lane & 3) == 0) {
+          sums.scale[which][r0] = s[0].s;
+          sums.scale[which][r1] = s[1].s;
+          sums.rel[which][r0] = __float2half_rn(s[0].s * sa.inv);
+          sums.rel[which][r1] = __float2half_rn(s[1].s * sa.inv);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (2 * half + (i >> 1) > m) break;  // nothing above the 16 x 16 diagonal blocks is read
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t hi, lo;
+            split2(y[i][2 * e], y[i][2 * e + 1], s[e].inv, hi, lo);
+            uint8_t *to = smem + Sm::kU + 2 * which * kTriBytes + tile_off(e ? r1 : r0, 4 * half + i) + 2 * col;
+            *reinterpret_cast<uint32_t *>(to) = hi;
+            *reinterpret_cast<uint32_t *>(to + kTriBytes) = lo;
+          }
+        }
+      }
+      if (lane < 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) sums.cols[m][32 * half + 8 * i + col + e] = cs[i][e];
       if ((lane & 3) == 0) {
         sums.rows[half][r0] = rg0;
         sums.rows[half][r1] = rg1;
@@ -1096,15 +1134,23 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
       if (lane == 0) sums.cross[warp] = cross;
       __syncthreads();
 
-      auto times = [&](uint32_t plane, bool transposed, uint32_t tile, float f, float (&out)[NH][4]) {
+      auto times = [&](int which, bool transposed, uint32_t tile, float f, float (&out)[NH][4]) {
         zero(z);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
           if (transposed ? kk < m : kk > m) continue;
           uint32_t hi[4], lo[4];
+          const uint32_t plane = sb + Sm::kU + 2 * which * kTriBytes;
           if (transposed) {
             load_at(hi, plane, 16 * m, 16 * kk);
             load_at(lo, plane + kTriBytes, 16 * m, 16 * kk);
+            const __half2 ra = *reinterpret_cast<const __half2 *>(&sums.rel[which][16 * kk + col]);
+            const __half2 rb = *reinterpret_cast<const __half2 *>(&sums.rel[which][16 * kk + 8 + col]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              hi[i] = times2(hi[i], i < 2 ? ra : rb);
+              lo[i] = times2(lo[i], i < 2 ? ra : rb);
+            }
           } else {
             load_a(hi, plane, 16 * m, 16 * kk);
             load_a(lo, plane + kTriBytes, 16 * m, 16 * kk);
@@ -1119,15 +1165,17 @@ gdr_local_kernel(const Tin *__restrict__ v, const float *__restrict__ g,
             mma(z[2 * np + 1], lo, b[2], b[3]);
           }
         }
+        const float f0 = f * sums.scale[which][transposed ? C : r0];
+        const float f1 = f * sums.scale[which][transposed ? C : r1];
 #pragma unroll
         for (int i = 0; i < NH; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) out[i][e] = fmaf(f, z[i][e], out[i][e]);
+          for (int e = 0; e < 4; ++e) out[i][e] = fmaf(e >> 1 ? f1 : f0, z[i][e], out[i][e]);
       };
-      times(sb + Sm::kU, false, sb + Sm::kK, sw.s * ks, aq);
-      times(sb + Sm::kU, true, sb + Sm::kQ, sw.s * qs, ak);
-      times(sb + Sm::kU + 2 * kTriBytes, false, sb + Sm::kK, sn.s * ks, ak);
-      times(sb + Sm::kU + 2 * kTriBytes, true, sb + Sm::kK, sn.s * ks, ak);
+      times(0, false, sb + Sm::kK, ks, aq);
+      times(0, true, sb + Sm::kQ, qs, ak);
+      times(1, false, sb + Sm::kK, ks, ak);
+      times(1, true, sb + Sm::kK, ks, ak);
 
       if (warp == 0) {  // dg and dbeta of tokens 2 lane, 2 lane + 1
         double d[2], e = 0.0;

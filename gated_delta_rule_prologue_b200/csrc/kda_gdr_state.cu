@@ -167,11 +167,6 @@ gdr_state_kernel(const Tin *__restrict__ v, const float *s0, const int32_t *__re
     zero(qs);
     Scale a0, a1;
     row_scales(s, a0, a1);
-    if (kRole == kKeep && (lane & 3) == 0) {
-      float *p = reinterpret_cast<float *>(ws + lay.scales) + ((size_t)(slot0 + c) * HV + h) * 2 * D + row;
-      p[0] = a0.s;
-      p[8] = a1.s;
-    }
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       uint32_t hi[4], lo[4];

@@ -291,8 +291,6 @@ gdr_state_tc_kernel(const __grid_constant__ CUtensorMap tm_v, const float *s0,
                    (((size_t)(slot0 + c) * HV + h) * D + half * 64) * D + row;
 #pragma unroll
         for (int i = 0; i < D / 2; ++i) __stcs(p + i * D, s[i]);
-        if (half == 0)
-          reinterpret_cast<float *>(ws + lay.scales)[((size_t)(slot0 + c) * HV + h) * 2 * D + row] = ss.s;
       }
       if (!(ok = wait(&sm.full[par], (c >> 1) & 1, sm, status))) break;
       if (warp == 0) {

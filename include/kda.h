@@ -596,8 +596,10 @@ kda_status kda_gdr_decode_step(const void *q, const void *k, const void *v, cons
  * and sizes (kda_gdr_chunk_fwd_workspace_bytes is 0 then) the call is
  * kda_gdr_recurrent.  Products run on the tensor cores on fp16 terms: q and k
  * exactly (bf16 values below 2^-14 of a 64-token tile's largest are off by up to
- * 2^-25 of it), every other operand as two terms of 11 bits each, so errors are
- * those of fp32 arithmetic relative to the largest values of a state row.  A NaN or
+ * 2^-25 of it), every other operand as two terms of 11 bits each.  So errors are
+ * those of fp32 arithmetic relative to the largest of a value channel, in the state
+ * and among the 64 tokens of a chunk: a token whose v is 2^-20 of another's in its
+ * chunk has a read-out that is exact to about 2^-22 of the other's.  A NaN or
  * an infinity of a token reaches the earlier rows of its own 64-token chunk too, which
  * are sums with it times zero; chunks before it, other heads and other sequences stay
  * as they are, and so do other channels if it is one of v.
@@ -622,7 +624,10 @@ kda_status kda_gdr_chunk_fwd_ws(const void *q, const void *k, const void *v, con
  *   workspace        >= kda_gdr_chunk_bwd_workspace_bytes(...) bytes, 16-byte
  *                    aligned, caller-owned, not NULL
  * Supported: dt KDA_BF16 or KDA_F16, D 64 or 128, T > 0, else KDA_ERR_UNSUPPORTED.
- * Rows of tokens outside every sequence are not written.
+ * Rows of tokens outside every sequence are not written.  Errors are those of fp32
+ * arithmetic: in dq relative to what a token's own d_o makes of the largest of S and
+ * U, key channel by key channel; in the other gradients relative to the largest of
+ * the 64 tokens of a chunk, value channel by value channel.
  */
 size_t kda_gdr_chunk_bwd_workspace_bytes(int N, int T, int HK, int HV, int D, kda_dtype dt);
 kda_status kda_gdr_chunk_bwd_ws(const void *q, const void *k, const void *v, const float *g,
