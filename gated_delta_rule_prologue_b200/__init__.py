@@ -672,8 +672,9 @@ def kda_output_epilogue(o, gate, weight, out, *, eps: float = 1e-5, stream=None)
 # step's kernel takes three microseconds, so a call's checks are one expression that reads each
 # attribute once; where it fails, _p looks at the tensors one by one and names what is wrong.
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# None on a torch without CUDA, where no call gets past its checks.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _p(t, name, shape, dtype, device):

@@ -1,6 +1,9 @@
 """Argument checks of the kda_gdr_* entry points and of the backward passes of the prologue and
 the output epilogue, without a GPU: every call here is refused before anything is launched."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -216,3 +219,27 @@ def test_chunk_forward_refuses_less_than_the_records(kda):
     assert f(1, 4000, 1, 2, 128, 1) > records
     refused(kda, gdr(kda, "kda_gdr_chunk_fwd_ws", N=1, T=4000, HK=1, HV=2, nbytes=records - 1), 1,
             b"workspace holds %d bytes, these sizes need %d" % (records - 1, records))
+
+
+def test_loads_on_a_torch_without_cuda(kda):
+    """Where torch has no CUDA functions the module loads and its calls refuse what they are given."""
+    code = """
+import torch
+for name in [n for n in dir(torch._C) if n.startswith("_cuda_")]:
+    delattr(torch._C, name)
+import gated_delta_rule_prologue_b200 as kda
+x = torch.zeros(4, 2, 64)
+for call in (lambda: kda.kda_gdr_recurrent(x, x, x, x[..., 0], x[..., 0], x),
+             lambda: kda.kda_chunk_fwd(x, x, x, x, x[..., 0].contiguous(), x),
+             lambda: kda.kda_output_epilogue_bwd(x, x, x[0, 0], x, x, x)):
+    try:
+        call()
+    except ValueError as e:
+        assert "CUDA" in str(e), e
+    else:
+        raise AssertionError("not refused")
+print("loaded")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0 and "loaded" in r.stdout, r.stderr[-2000:]
