@@ -1,4 +1,4 @@
-"""Gradients of the chunked one-decay rule row by row: what one token, or one key channel, gets is as
+"""The chunked one-decay rule row by row: what one token, or one key channel, gets is as
 exact for itself where others of the same 64-token chunk are larger by many powers of two.
 
 dq of a token is made of its own d_o alone, with the state's key channels and the other tokens' keys and
@@ -14,7 +14,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_gdr import BF16, CHUNK, DEV, HALF_STEP, Problem, check_backward, close, f64, kda
+from test_gpu_gdr import BF16, CHUNK, DEV, F16, Problem, check_backward, close, f64, kda
 
 pytestmark = pytest.mark.gpu
 __all__ = ["kda"]  # the fixture
@@ -78,3 +78,24 @@ def test_gradients_of_any_size(kda, power):
     p.d_o, p.d_sN = p.d_o * 2.0 ** power, p.d_sN * 2.0 ** power
     for a, b in zip(p.backward(kda), one):
         assert torch.equal(a.float(), b.float() * 2.0 ** power)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+def test_read_out_of_tokens_with_small_queries_and_keys(kda, dtype, D):
+    """Queries and keys of norms from 2^-8 to 1 in one chunk: a token's read-out for its query's size.
+
+    fp16 inputs are exact.  bf16 values below 2^-14 of the tile's largest are off by 2^-25 of it: in a
+    query of norm 2^-8 that is the twentieth of its values below 2^-6 of its largest (a quarter to a third
+    of its norm), and the read-out is off by sqrt(128 / 20) * 2^-25 * 0.35 / sqrt(3) * 2^8 = 4e-6 of its
+    RMS, five times that at worst, 2e-5 beside CHUNK."""
+    T = 150
+    r = torch.Generator().manual_seed(D)
+    size, ksize = (2.0 ** -torch.randint(0, 9, (T,), generator=r) for _ in range(2))
+    p = Problem([T], 2, 4, D, dtype, seed=D,
+                qk=lambda q, k: (q * size[:, None, None], k * ksize[:, None, None]))
+    p.forward(kda.kda_gdr_chunk_fwd)
+    o, last = p.reference()
+    size = size.double().numpy()[:, None, None]
+    close("o for its size", f64(p.o) / size, o / size, CHUNK + 2e-5)
+    close("state", p.sN, last, CHUNK + 2e-5)
