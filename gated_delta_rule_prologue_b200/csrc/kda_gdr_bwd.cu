@@ -23,9 +23,9 @@
 // pass about 1000 per warp (8 warps); a chunk of the local pass reads 270 KB.  The local pass keeps S and dS' as split
 // fp16 rows in shared memory (128 KB) with K, Q, U and dO or X, one persistent CTA per SM.
 // Bounds: the reverse pass a chain's latency, 5.6 us a chunk (64 chains of 32 chunks on 128 SMs: 180 us);
-// the local pass the latency of its steps with two warps per SM quarter (the tensor pipe is busy about 36%
-// of the time, 30% of the issue slots), 25 us a chunk and SM: 2048 chunks 350 us, 629 MB.  372 us with the
-// scales, g and beta loaded when an item starts instead of one ahead; 428 with 16 warps per CTA then.
+// the local pass the latency of its steps with two warps per SM quarter (the tensor pipe is busy 34% of the
+// time, 30% of the issue slots), 27 us a chunk and SM: 2048 chunks 371 us, 629 MB.  16 warps per CTA took
+// 15% longer; one scale for all of W or M and of S or dS' instead of one per row would save 4%.
 #include "kda_gdr.cuh"
 #include "kda_tcgen05.cuh"
 

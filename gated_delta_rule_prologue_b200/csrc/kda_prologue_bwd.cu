@@ -21,9 +21,10 @@
 //
 // Bytes: x + dx + dn (6 per channel and token for 16-bit types), plus 3 halo rows per tile served by
 // L2.  8192 tokens, 32 heads of 128 in bf16: 158 us with the weights' second kernel, 604 MB, 3.8 TB/s.
-// Bound by instruction issue with four warps per scheduler (about 150 a token and warp before the steps
-// without looks at the stretch's ends, 62% of the issue slots; 168 us).  The rows fetched to shared
-// memory instead, eight or twelve tokens ahead, no register spilled: 164 and 161 us.
+// Bound by latency with the four warps per scheduler that 128 registers leave: 54% of the issue slots, 43%
+// of DRAM; a warp issues every 6.8 cycles (fixed latencies 1.5, loads 1.0, math pipe 0.9, shuffles 0.8).
+// 168 us with looks at the stretch's ends in every step.  The rows fetched to shared memory instead,
+// eight or twelve tokens ahead, no register spilled: 164 and 161 us.
 #include <type_traits>
 
 #include "kda_common.cuh"
