@@ -16,10 +16,11 @@
 // other operand (state, U, T, P, gradients) is split in two fp16 terms, x 2^-e = hi + lo, with a
 // power of two per row that puts the row's largest value in [1, 2): 22 significant bits below that,
 // so a product's errors are those of fp32 arithmetic on rows whose values are all as large as their
-// largest, and no value of the fp32 range overflows.  Rows are, in the state passes, a value channel over
-// the key channels or over the chunk's 64 tokens; in the local pass a token over the channels (dO, X, U)
-// or over the chunk's tokens (W, M), and a key channel over the value channels (S, dS').  A product of a
-// split operand with an exact one takes two MMAs, of two split ones three (hi hi, hi lo, lo hi).
+// largest, and no value of the fp32 range overflows.  A row is a token over the chunk's tokens (T, P, and
+// the local pass's W and M); in the state passes a value channel over the key channels or over the
+// chunk's 64 tokens; in the local pass a token over the channels (dO, X, U) and a key channel over the
+// value channels (S, dS').  A product of a split operand with an exact one takes two MMAs, of two split
+// ones three (hi hi, hi lo, lo hi).
 //
 // Workspace: records of the chunks.  Chunk c of sequence n, whose first token is bos, has slot
 // bos / 64 + n + c (strictly increasing from chunk to chunk, so no index pass is needed; T / 64 +
